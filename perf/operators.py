@@ -6,9 +6,9 @@ factors.
             y = x rstd gamma (RMS norm), with the row statistics
   norm_bwd  dx, dgamma, dbeta from one to four gradients of y, one for each
             projection that read y
-  fp8_fwd   Y = Q(X) W^T, where Q rounds each 128-wide block of a row to e4m3
-            with a power-of-two scale and W is e4m3 with a float32 scale for
-            each 128 x 128 block
+  fp8_fwd   Y = Q(X) W^T in bf16, where Q rounds each 128-wide block of a row
+            to e4m3 with a power-of-two scale and W is e4m3 with a float32
+            scale for each 128 x 128 block
   fp8_dx    dX = Q(dY) W, the same W read in its own layout
   orth      Newton-Schulz orthogonalisation of a batch of matrices
   muon      momentum, orthogonalisation and the update of the parameters
@@ -41,8 +41,8 @@ def listed():
         {"name": "norm bwd 4096x2560 rms", "op": "norm_bwd", "kind": "rms", "rows": 4096, "dim": 2560, "dtype": "f32", "grads": 3},
         # One token through a query projection: the weight's bytes are the cost.
         {"name": "fp8 fwd 1x2560x4096", "op": "fp8_fwd", "tokens": 1, "in_dim": 2560, "out_dim": 4096, "dtype": "f32"},
-        # A ragged chunk through a ragged weight, bf16 result.
-        {"name": "fp8 fwd 1000x2056x1368 bf16", "op": "fp8_fwd", "tokens": 1000, "in_dim": 2056, "out_dim": 1368, "dtype": "bf16"},
+        # A ragged chunk through a ragged weight, bf16 activations.
+        {"name": "fp8 fwd 1000x2056x1368", "op": "fp8_fwd", "tokens": 1000, "in_dim": 2056, "out_dim": 1368, "dtype": "bf16"},
         # The widest frozen product of a Qwen3-4B-shaped layer, one chunk.
         {"name": "fp8 fwd 4096x2560x9728", "op": "fp8_fwd", "tokens": 4096, "in_dim": 2560, "out_dim": 9728, "dtype": "f32"},
         # Its gradient, over a chunk of the two-slot workload.
@@ -127,7 +127,7 @@ def prepare(case, seed):
         q = (tiles / scale[:, None, :, None]).view(nb * 128, kb * 128).to(torch.float8_e4m3fn)
         buf = torch.cat([q.view(torch.uint8).flatten(), scale.flatten().view(torch.uint8)])
         x = _activations(g, t, k) if op == "fp8_fwd" else 1e-2 * torch.exp(0.5 * _rand(g, t, 1)) * _rand(g, t, n)
-        return {"case": case, "x": x, "w": buf}
+        return {"case": case, "x": x.to(_type(case)), "w": buf}
     # Gradients of a low-rank factor: a few strong directions over noise.
     b, m, n = case["count"], case["rows"], case["cols"]
     r = min(m, n)
@@ -187,8 +187,8 @@ def _rounded(x):
 
 def _fp8(s):
     w = _weight(s)
-    y = torch.matmul(_rounded(s["x"]), w.t() if s["case"]["op"] == "fp8_fwd" else w)
-    return y.to(_type(s["case"]))
+    y = torch.matmul(_rounded(s["x"].float()), w.t() if s["case"]["op"] == "fp8_fwd" else w)
+    return y.to(torch.bfloat16)
 
 
 def _ns_step(x):
@@ -236,7 +236,7 @@ def _own(s):
         w = L.Fp8Weight(case["out_dim"], case["in_dim"], s["w"])
         q = L.fp8_rows(*s["x"].shape)
         L.lora_fp8_quantize(s["x"], q)
-        y = torch.empty(case["tokens"], case["out_dim"] if op == "fp8_fwd" else case["in_dim"], device="cuda", dtype=_type(case))
+        y = torch.empty(case["tokens"], case["out_dim"] if op == "fp8_fwd" else case["in_dim"], device="cuda", dtype=torch.bfloat16)
         L.lora_fp8_product(q, w, y, dx=op == "fp8_dx")
         return y
     runs = [L.make_matrix_run(0, case["rows"], case["cols"], case["count"])]
@@ -274,7 +274,7 @@ def work(case):
         t, k, n = case["tokens"], case["in_dim"], case["out_dim"]
         rd, wr = (k, n) if op == "fp8_fwd" else (n, k)
         scales = 4 * -(-k // 128) * -(-n // 128)
-        return {"bytes": 4 * t * rd + k * n + scales + (2 if case["dtype"] == "bf16" else 4) * t * wr, "flops": 2 * t * k * n}
+        return {"bytes": (2 if case["dtype"] == "bf16" else 4) * t * rd + k * n + scales + 2 * t * wr, "flops": 2 * t * k * n}
     size, r = case["count"] * case["rows"] * case["cols"], min(case["rows"], case["cols"])
     # Two products with the matrix (its Gram matrix, half of it by symmetry,
     # and the polynomial times it) and the polynomial's small ones.
