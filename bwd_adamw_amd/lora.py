@@ -26,6 +26,8 @@ __all__ = [
     "lora_slots_workspace_bytes", "lora_forward_slots", "lora_backward_slots",
     "lora_qweight_layout", "lora_grad_prepare_noalloc",
     "lora_dora_row_norms_batch_workspace_bytes", "lora_dora_row_norms_batch", "QWeight", "qweight_pack", "Q_FORMATS", "EXPORTS", "GroupCall",
+    "LoraNorm", "make_norm", "lora_norm_forward", "lora_norm_workspace_bytes",
+    "lora_norm_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblora.so")
@@ -48,6 +50,7 @@ EXPORTS = (
     "lora_slots_workspace_bytes", "lora_forward_slots", "lora_backward_slots",
     "lora_qweight_layout", "lora_grad_prepare_noalloc",
     "lora_dora_row_norms_batch_workspace_bytes", "lora_dora_row_norms_batch",
+    "lora_norm_forward", "lora_norm_workspace_bytes", "lora_norm_backward",
 )
 
 
@@ -83,6 +86,12 @@ class LoraAdamwHparams(C.Structure):
     _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double),
                 ("eps", C.c_double), ("weight_decay", C.c_double), ("plus_ratio", C.c_double),
                 ("t", C.c_int64)]
+
+
+class LoraNorm(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("dim", C.c_int64), ("ldx", C.c_int64), ("ldy", C.c_int64),
+                ("kind", C.c_int32), ("dtype", C.c_int32), ("gamma", C.c_void_p),
+                ("beta", C.c_void_p), ("eps", C.c_float)]
 
 
 _LIB = None
@@ -124,6 +133,9 @@ def lib() -> C.CDLL:
             "lora_qweight_layout": (SZ, [I32, I64, I64, P]),
             "lora_dora_row_norms_batch_workspace_bytes": (SZ, [I32, P]),
             "lora_dora_row_norms_batch": (I32, [I32, P, P, P, SZ, P]),
+            "lora_norm_forward": (I32, [P, P, P, P, P]),
+            "lora_norm_workspace_bytes": (SZ, [P]),
+            "lora_norm_backward": (I32, [P, P, I32, P, P, P, P, P, I32, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -569,6 +581,84 @@ def lora_merge(lin: LoraLinear, W_out, rmse=None, ws=None, stream=None):
                           _sized(rmse, "rmse", 1, torch.float64), _ptr(ws, "ws", None), ws_bytes,
                           _stream(stream))
     _check("lora_merge", rc)
+
+
+# --------------------------------------------------------------- row norms
+NORM_KINDS = {"layer": 0, "rms": 1}
+_ACT_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _act(dtype) -> int:
+    if dtype not in _ACT_DTYPES:
+        raise TypeError(f"activations must be float32 or bfloat16, got {dtype}")
+    return _ACT_DTYPES[dtype]
+
+
+def make_norm(kind, rows, dim, dtype=torch.float32, eps=1e-5, gamma=None, beta=None, ldx=None,
+              ldy=None) -> LoraNorm:
+    """Descriptor of a row norm ("layer" or "rms") over X [rows, dim]; ldx and
+    ldy are the elements between rows of X, dX and of Y, dY (default dim)."""
+    if kind not in NORM_KINDS:
+        raise ValueError(f"norm kind must be one of {sorted(NORM_KINDS)}, got {kind!r}")
+    dt = _act(dtype)
+    return LoraNorm(int(rows), int(dim), int(dim if ldx is None else ldx),
+                    int(dim if ldy is None else ldy), NORM_KINDS[kind], dt,
+                    _sized(gamma, "gamma", int(dim)), _sized(beta, "beta", int(dim)), float(eps))
+
+
+def _rows_ptr(t, name, rows, dim, ld, dtype):
+    """Device pointer of a [rows, dim] tensor whose rows are ld elements
+    apart (a column slice of a wider matrix, say)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if _act(t.dtype) != dtype:
+        raise TypeError(f"{name} must be {'float32' if dtype == F32 else 'bfloat16'}, got {t.dtype}")
+    if tuple(t.shape) != (rows, dim):
+        raise ValueError(f"{name} must be [{rows}, {dim}], got {list(t.shape)}")
+    if (dim > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != ld):
+        raise ValueError(f"{name} must have strides [{ld}, 1], got {list(t.stride())}")
+    return t.data_ptr()
+
+
+def lora_norm_forward(norm: LoraNorm, X, Y, stats=None, stream=None):
+    """Y = norm(X); stats [rows, 2] float32 receives each row's mean and rstd."""
+    r, d = norm.rows, norm.dim
+    rc = lib().lora_norm_forward(C.byref(norm), _rows_ptr(X, "X", r, d, norm.ldx, norm.dtype),
+                                 _rows_ptr(Y, "Y", r, d, norm.ldy, norm.dtype),
+                                 _sized(stats, "stats", 2 * r), _stream(stream))
+    _check("lora_norm_forward", rc)
+
+
+def lora_norm_workspace_bytes(norm: LoraNorm) -> int:
+    return int(lib().lora_norm_workspace_bytes(C.byref(norm)))
+
+
+def lora_norm_backward(norm: LoraNorm, X, dY, stats, dX=None, dgamma=None, dbeta=None,
+                       accumulate=False, ws=None, stream=None):
+    """Gradients of lora_norm_forward from the gradients of Y in the list dY
+    (one to four, summed).  A workspace is taken from torch's allocator when
+    dgamma or dbeta is wanted and `ws` is None."""
+    r, d, dt = norm.rows, norm.dim, norm.dtype
+    if not 1 <= len(dY) <= MAX_GROUP:
+        raise ValueError(f"dY must hold 1 to {MAX_GROUP} gradients, got {len(dY)}")
+    dys = (C.c_void_p * len(dY))(*[_rows_ptr(t, f"dY[{i}]", r, d, norm.ldy, dt)
+                                   for i, t in enumerate(dY)])
+    if ws is None and (dgamma is not None or dbeta is not None):
+        need = lora_norm_workspace_bytes(norm)
+        if need:
+            ws = torch.empty(need, device=X.device, dtype=torch.uint8)
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    rc = lib().lora_norm_backward(C.byref(norm), _rows_ptr(X, "X", r, d, norm.ldx, dt), len(dY),
+                                  dys, _sized(stats, "stats", 2 * r),
+                                  _rows_ptr(dX, "dX", r, d, norm.ldx, dt),
+                                  _sized(dgamma, "dgamma", d), _sized(dbeta, "dbeta", d),
+                                  1 if accumulate else 0, _ptr(ws, "ws", None), ws_bytes,
+                                  _stream(stream))
+    _check("lora_norm_backward", rc)
 
 
 def lora_set_bf16_config(cfg: int):

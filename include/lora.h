@@ -356,6 +356,48 @@ size_t lora_merge_workspace_bytes(const lora_linear* lin);
 int lora_merge(const lora_linear* lin, void* W_out, int out_dtype, double* rmse, void* workspace,
                size_t workspace_bytes, void* stream);
 
+/* Row norms: the layer norm or RMS norm whose output is the X that a group of
+ * adapted linears reads, over rows of X [rows, dim].  With mean_t the row's
+ * mean (0 for RMS), rstd_t = 1 / sqrt(mean_k (x - mean_t)^2 + eps) and
+ * xh = (x - mean_t) rstd_t:
+ *   y = xh gamma + beta
+ *   dx = rstd_t (g - [layer] mean_k g - xh mean_k (g xh)),  g = dy gamma
+ *   dgamma (+)= sum_t dy xh,   dbeta (+)= sum_t dy
+ * The variance is taken of the centred values; everything between the loads
+ * and the one rounding of Y or dX is float32, the sums over rows float32
+ * within a block of rows and double over the blocks, in a fixed order.
+ * X, Y, dY and dX share one element type, LORA_F32 or LORA_BF16, and have
+ * rows ldx (X, dX) and ldy (Y, dY) elements apart.  Any element alignment and
+ * any dim up to 16384 are accepted (LORA_E_SHAPE past it); rows whose starts
+ * are 16-byte (bf16: 8-byte) aligned with dim a multiple of 4 run faster. */
+typedef enum lora_norm_kind {
+  LORA_NORM_LAYER = 0,
+  LORA_NORM_RMS = 1
+} lora_norm_kind;
+typedef struct lora_norm {
+  int64_t rows, dim;
+  int64_t ldx, ldy;         /* elements between rows, >= dim               */
+  int32_t kind;             /* lora_norm_kind                              */
+  int32_t dtype;            /* LORA_F32 or LORA_BF16                       */
+  const float* gamma;       /* [dim] or NULL (ones)                        */
+  const float* beta;        /* [dim] or NULL (zeros); RMS ignores it       */
+  float eps;                /* >= 0                                        */
+} lora_norm;
+
+/* stats [rows, 2] (8-byte aligned) receives mean and rstd of each row for the
+ * backward; NULL skips it.  Y may be X itself when ldx == ldy. */
+int lora_norm_forward(const lora_norm* norm, const void* X, void* Y, float* stats, void* stream);
+
+/* dY holds n_dy (1..LORA_MAX_GROUP) gradients of Y, added as they are read:
+ * the dX of a group's linears.  stats is the forward's.  dX (overwritten),
+ * dgamma and dbeta may be NULL, not all three; dbeta needs a layer norm.
+ * accumulate != 0 adds into dgamma and dbeta.  ws: lora_norm_workspace_bytes
+ * when dgamma or dbeta is wanted, else it may be NULL. */
+size_t lora_norm_workspace_bytes(const lora_norm* norm);
+int lora_norm_backward(const lora_norm* norm, const void* X, int n_dy, const void* const* dY,
+                       const float* stats, void* dX, float* dgamma, float* dbeta, int accumulate,
+                       void* ws, size_t ws_bytes, void* stream);
+
 /* Diagnostics: launch timing.  lora_profile_begin opens a profile that can
  * hold max_launches launches (it creates that many HIP event pairs once and
  * keeps them); until lora_profile_end, each kernel launch of the library is
