@@ -1,0 +1,569 @@
+// Newton-Schulz orthogonalisation of matrices with one short side, and the
+// momentum update that uses it.
+//
+// With X_0 = u / (||u||_F + eps) and R the short side, a step is
+//   X_{k+1} = Q_k X_k,  Q_k = a I + b G_k + c G_k^2,  G_k = X_k X_k^T  (R x R).
+// Every Q_k is a polynomial of G_0, so all of them commute and
+//   X_n = P X_0,  P = Q_{n-1} ... Q_0,   G_{k+1} = Q_k G_k Q_k:
+// the iteration needs the data only for G_0 and for the last product.  (A
+// tall matrix is the transpose: G_0 = X^T X, X_n = X P.)  Three launches:
+//   gram   u from the gradient and the momentum (which it updates), and the
+//          upper half of u u^T by blocks of columns; reads g, m, writes m
+//   poly   one block a matrix: sums the blocks' partials in order, takes the
+//          norm from the trace, iterates Q and G in LDS, leaves P
+//   apply  P u and the parameter update; reads g, m, p, writes p
+// against the 2 n passes over X of the iteration as written.
+//
+// The products run on float64 MFMA (16x16x4).  P reaches a^n (485 for the
+// usual a and five steps) where a singular value is small, and an error e of
+// G_0 there becomes P e X: with float32 sums of G a spectrum wider than 1e3
+// would lose all but three digits.  In float64 the results are as accurate as
+// the float32 data, and the two passes still cost less MFMA time than memory
+// time up to R = 128 (2 R flops an element each, the first half of that by
+// symmetry, at 64 flops a byte and more).
+//
+// Fragments: a 16x16x4 operand is row l % 16 and contraction index l / 16 of
+// lane l, the same for both sides of a symmetric product, so one load serves
+// both.  Which element a lane calls its "row" and which contraction index a
+// lane group takes is free as long as the sides agree: wide matrices take
+// four neighbouring columns a lane (16-byte loads), tall ones RP / 16
+// neighbouring columns a lane as RP / 16 fragments.  The result's row is
+// 4 v + l / 16 for value v (not 4 (l / 16) + v as in float32).
+#pragma once
+#include "common.hpp"
+
+namespace lora {
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+LORA_DEV f64x4 mfma16x16x4_f64(double a, double b, f64x4 c) {
+  return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+}
+
+constexpr int MUON_MAX_RUNS = 32;
+struct MuonRun {
+  int64_t offset, stride;    // first matrix, elements between matrices
+  int32_t rows, cols, count;
+  int32_t splits;            // blocks a matrix (gram and apply)
+  int32_t len;               // long-side length of a block's range
+  int32_t mat0;              // index of its first matrix among the call's
+  int32_t blk0;              // first block
+  float rate, decay;         // lr factor, lr weight decay
+};
+struct MuonArgs {
+  MuonRun run[MUON_MAX_RUNS];
+  int nruns;
+  const float* G;        // gradient arena
+  float* M;              // momentum arena (NULL: orthogonalise G alone)
+  float* P;              // parameter arena, or the result of an orthogonalisation
+  const float* d_scale;  // or NULL
+  double* part;          // [block][tiles][64][4]
+  double* poly;          // [matrix][RP][RP]
+  float mu;
+  int nesterov;
+  int steps;
+  double eps, a, b, c;
+};
+
+// The run that block (or, by `mats`, matrix) index b falls in.
+LORA_DEV int muon_find(const MuonArgs& p, int b, bool mats) {
+  int r = 0;
+  for (int i = 1; i < p.nruns; ++i)
+    if ((mats ? p.run[i].mat0 : p.run[i].blk0) <= b) r = i;
+  return __builtin_amdgcn_readfirstlane(r);
+}
+
+LORA_DEV bool muon_vetoed(const MuonArgs& p) {
+  return p.d_scale && !(fabsf(*p.d_scale) <= 3.402823466e38f);
+}
+
+// N (1, 2 or 4) neighbouring values at element `at` of a matrix (under 2^30
+// elements: a scalar base and a 32-bit byte offset), of which the first n
+// exist.
+template <bool VEC, int N>
+LORA_DEV void ldn(float* v, const float* base, uint32_t at, int n) {
+  const float* p = reinterpret_cast<const float*>(reinterpret_cast<const char*>(base) + 4u * at);
+  if constexpr (VEC && N == 4) {
+    const f32x4 t = n > 0 ? *reinterpret_cast<const f32x4*>(p) : f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = t[e];
+  } else if constexpr (VEC && N == 2) {
+    const f32x2 t = n > 0 ? *reinterpret_cast<const f32x2*>(p) : f32x2{0, 0};
+    v[0] = t[0];
+    v[1] = t[1];
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = e < n ? p[e] : 0.0f;
+  }
+}
+template <bool VEC, int N>
+LORA_DEV void stn(const float* v, float* base, uint32_t at, int n) {
+  float* p = reinterpret_cast<float*>(reinterpret_cast<char*>(base) + 4u * at);
+  if constexpr (VEC && N == 4) {
+    if (n > 0) *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+  } else if constexpr (VEC && N == 2) {
+    if (n > 0) *reinterpret_cast<f32x2*>(p) = f32x2{v[0], v[1]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < n) p[e] = v[e];
+  }
+}
+
+// u of one element, from the gradient and the momentum after its update.
+LORA_DEV float muon_u(const MuonArgs& p, float g, float m) {
+  return p.nesterov ? fmaf(p.mu, m, g) : m;
+}
+
+// A chunk of the long side as gram reads it: NK contraction steps of four
+// indices, one per lane group, for each of the F fragments.
+template <int RP, bool WIDE, bool VEC, bool MUON>
+struct GramChunk {
+  static constexpr int F = RP / 16;
+  static constexpr int NK = RP >= 64 ? 4 : 8;   // 16 or 32 long-side indices
+  static constexpr int LEN = 4 * NK;
+  float g[F][NK], m[MUON ? F : 1][MUON ? NK : 1];
+
+  // Each access: fragment f (wide) or group of Q fragments (tall).
+  static constexpr int Q = WIDE ? 4 : (F > 4 ? 4 : F);
+
+  template <typename Fn>
+  LORA_DEV static void each(const MuonRun& r, int k0, int k1, int lane, Fn fn) {
+    const int c = lane & 15, h = lane >> 4;
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int q = 0; q < NK / 4; ++q) {
+          const int row = 16 * f + c;
+          const int k = k0 + 16 * q + 4 * h;
+          fn(f, 4 * q, (uint32_t)row * (uint32_t)r.cols + (uint32_t)k,
+             row < r.rows && k < k1 ? min(4, k1 - k) : 0);
+        }
+    } else {
+#pragma unroll
+      for (int s = 0; s < NK; ++s)
+#pragma unroll
+        for (int f = 0; f < F; f += Q) {
+          const int k = k0 + 4 * s + h;
+          const int col = F * c + f;
+          fn(f, s, (uint32_t)k * (uint32_t)r.cols + (uint32_t)col, k < k1 && col < r.cols ? min(Q, r.cols - col) : 0);
+        }
+    }
+  }
+  LORA_DEV void load(const MuonArgs& p, const MuonRun& r, int64_t base, int k0, int k1, int lane) {
+    each(r, k0, k1, lane, [&](int f, int s, uint32_t at, int n) {
+      float v[Q];
+      ldn<VEC, Q>(v, p.G + base, at, n);
+#pragma unroll
+      for (int e = 0; e < Q; ++e) (WIDE ? g[f][s + e] : g[f + e][s]) = v[e];
+      if constexpr (MUON) {
+        ldn<VEC, Q>(v, p.M + base, at, n);
+#pragma unroll
+        for (int e = 0; e < Q; ++e) (WIDE ? m[f][s + e] : m[f + e][s]) = v[e];
+      }
+    });
+  }
+  // The momentum's update (done before this kernel where waves share their
+  // chunks, RP 128); g becomes u.
+  LORA_DEV void update(const MuonArgs& p, const MuonRun& r, int64_t base, int k0, int k1, int lane,
+                       float sc) {
+    if constexpr (MUON) {
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int s = 0; s < NK; ++s) {
+          const float gs = g[f][s] * sc;
+          if constexpr (RP < 128) m[f][s] = fmaf(p.mu, m[f][s], gs);
+          g[f][s] = muon_u(p, gs, m[f][s]);
+        }
+      if constexpr (RP < 128) each(r, k0, k1, lane, [&](int f, int s, uint32_t at, int n) {
+        float v[Q];
+#pragma unroll
+        for (int e = 0; e < Q; ++e) v[e] = WIDE ? m[f][s + e] : m[f + e][s];
+        stn<VEC, Q>(v, p.M + base, at, n);
+      });
+    }
+  }
+};
+
+template <int RP>
+constexpr int muon_tiles() {
+  return (RP / 16) * (RP / 16 + 1) / 2;
+}
+
+// Upper tile index -> (row tile, column tile), rows first.
+template <int RP>
+LORA_DEV void muon_tile(int i, int& t, int& u) {
+  t = 0;
+  int n = RP / 16;
+  while (i >= n) {
+    i -= n;
+    --n;
+    ++t;
+  }
+  u = t + i;
+}
+
+// Parts that the waves of a block split the result's tiles into: at RP 128
+// the 36 upper tiles (288 registers) are shared by two waves a chunk.
+template <int RP>
+constexpr int muon_parts() {
+  return RP == 128 ? 2 : 1;
+}
+template <int RP>
+constexpr int muon_part_tiles() {
+  return muon_tiles<RP>() / muon_parts<RP>();
+}
+
+// PART's tiles (i % parts == PART) over the chunks of wave kw.
+template <int RP, bool WIDE, bool VEC, bool MUON, int PART>
+LORA_DEV void gram_range(const MuonArgs& p, const MuonRun& r, int64_t base, int k0, int k1, int kw,
+                         float sc, f64x4 (&acc)[muon_part_tiles<RP>()]) {
+  typedef GramChunk<RP, WIDE, VEC, MUON> Chunk;
+  constexpr int F = Chunk::F, NP = muon_parts<RP>(), KW = 4 / NP;
+  const int lane = threadIdx.x & 63;
+  Chunk cur;
+  int k = k0 + kw * Chunk::LEN;
+  if (k >= k1) return;
+  cur.load(p, r, base, k, k1, lane);
+  for (;;) {
+    const int kn = k + KW * Chunk::LEN;
+    Chunk next;
+    if (kn < k1) next.load(p, r, base, kn, k1, lane);
+    cur.update(p, r, base, k, k1, lane, sc);
+#pragma unroll
+    for (int s = 0; s < Chunk::NK; ++s) {
+      double x[F];
+#pragma unroll
+      for (int f = 0; f < F; ++f) x[f] = (double)cur.g[f][s];
+      int i = 0;
+#pragma unroll
+      for (int t = 0; t < F; ++t)
+#pragma unroll
+        for (int u = t; u < F; ++u, ++i)
+          if (i % NP == PART) acc[i / NP] = mfma16x16x4_f64(x[t], x[u], acc[i / NP]);
+    }
+    if (kn >= k1) break;
+    k = kn;
+    cur = next;
+  }
+}
+
+// RP 128 reads each chunk in two waves, so the momentum is updated ahead of
+// it: m <- mu m + g' of one block's range.
+template <bool VEC>
+__global__ __launch_bounds__(256) void muon_momentum_kernel(MuonArgs p) {
+  if (muon_vetoed(p)) return;
+  const float sc = *p.d_scale;
+  const MuonRun& r = p.run[muon_find(p, blockIdx.x, false)];
+  const int rel = blockIdx.x - r.blk0, mat = rel / r.splits, sp = rel % r.splits;
+  const uint32_t n = (uint32_t)r.rows * (uint32_t)r.cols;
+  const uint32_t per = (n / r.splits + 1024) / 1024 * 1024;
+  const uint32_t e0 = sp * per, e1 = min(n, e0 + per);
+  const int64_t base = r.offset + mat * r.stride;
+  for (uint32_t e = e0 + 4 * threadIdx.x; e < e1; e += 1024) {
+    const int k = (int)min(4u, e1 - e);
+    float g[4], m[4];
+    ldn<VEC, 4>(g, p.G + base, e, k);
+    ldn<VEC, 4>(m, p.M + base, e, k);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m[q] = fmaf(p.mu, m[q], g[q] * sc);
+    stn<VEC, 4>(m, p.M + base, e, k);
+  }
+}
+
+template <int RP, bool VEC, bool MUON>
+__global__ __launch_bounds__(256, RP == 128 ? 1 : 2) void muon_gram_kernel(MuonArgs p) {
+  constexpr int NT = muon_tiles<RP>(), NP = muon_parts<RP>(), NA = muon_part_tiles<RP>();
+  __shared__ f64x4 sum[NT * 64];
+  if (muon_vetoed(p)) return;
+  const float sc = p.d_scale ? *p.d_scale : 1.0f;
+  const int ri = muon_find(p, blockIdx.x, false);
+  const MuonRun& r = p.run[ri];
+  const int rel = blockIdx.x - r.blk0, mat = rel / r.splits, sp = rel % r.splits;
+  const bool wide = r.rows <= r.cols;
+  const int k0 = sp * r.len, k1 = min(wide ? r.cols : r.rows, k0 + r.len);
+  const int64_t base = r.offset + mat * r.stride;
+  f64x4 acc[NA];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) acc[i] = f64x4{0, 0, 0, 0};
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, part = wave % NP, kw = wave / NP;
+  if (part == 0) {
+    if (wide) gram_range<RP, true, VEC, MUON, 0>(p, r, base, k0, k1, kw, sc, acc);
+    else gram_range<RP, false, VEC, MUON, 0>(p, r, base, k0, k1, kw, sc, acc);
+  } else {
+    if (wide) gram_range<RP, true, VEC, MUON, NP - 1>(p, r, base, k0, k1, kw, sc, acc);
+    else gram_range<RP, false, VEC, MUON, NP - 1>(p, r, base, k0, k1, kw, sc, acc);
+  }
+  // The waves' sums, in wave order.
+  for (int w = 0; w < 4 / NP; ++w) {
+    if (kw == w) {
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+        f64x4& s = sum[(i * NP + part) * 64 + lane];
+        s = w ? s + acc[i] : acc[i];
+      }
+    }
+    __syncthreads();
+  }
+  f64x4* out = reinterpret_cast<f64x4*>(p.part) + (int64_t)blockIdx.x * NT * 64;
+  for (int i = threadIdx.x; i < NT * 64; i += 256) out[i] = sum[i];
+}
+
+// ------------------------------------------------------------------- poly
+// Symmetric RP x RP matrices, rows LD apart.  The padding puts the 32 lanes
+// of a half wave (eight rows, four columns) in different LDS banks.
+template <int RP>
+struct Sym {
+  static constexpr int LD = RP + 4;
+  double* p;
+  LORA_DEV double& at(int i, int j) const { return p[i * LD + j]; }
+};
+
+// Upper tile i of A B (A, B symmetric and commuting, so the product is too).
+template <int RP>
+LORA_DEV f64x4 sym_tile(const Sym<RP>& A, const Sym<RP>& B, int i, int lane) {
+  int t, u;
+  muon_tile<RP>(i, t, u);
+  const int c = lane & 15, h = lane >> 4;
+  f64x4 d = {0, 0, 0, 0};
+#pragma unroll 8
+  for (int s = 0; s < RP / 4; ++s)
+    d = mfma16x16x4_f64(A.at(16 * t + c, 4 * s + h), B.at(16 * u + c, 4 * s + h), d);
+  return d;
+}
+template <int RP>
+LORA_DEV void sym_store(const Sym<RP>& C, int i, f64x4 d, int lane) {
+  int t, u;
+  muon_tile<RP>(i, t, u);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int row = 16 * t + 4 * v + (lane >> 4), col = 16 * u + (lane & 15);
+    C.at(row, col) = d[v];
+    C.at(col, row) = d[v];
+  }
+}
+
+// LDS for RP <= 64 (four matrices, 139 KB at 64); device memory for 128,
+// whose four matrices (540 KB) stay in the block's L2.
+template <int RP>
+constexpr bool poly_lds() {
+  return RP <= 64;
+}
+template <int RP>
+constexpr int64_t poly_doubles() {
+  return 4 * (int64_t)RP * Sym<RP>::LD;
+}
+
+template <int RP>
+__global__ __launch_bounds__(256) void muon_poly_kernel(MuonArgs p, double* scratch) {
+  constexpr int NT = muon_tiles<RP>(), F = RP / 16, PER = (NT + 3) / 4;
+  __shared__ double lds[poly_lds<RP>() ? poly_doubles<RP>() : 1];
+  __shared__ double diag[RP];
+  if (muon_vetoed(p)) return;
+  double* mem = poly_lds<RP>() ? lds : scratch + blockIdx.x * poly_doubles<RP>();
+  constexpr int64_t SZ = (int64_t)RP * Sym<RP>::LD;
+  const Sym<RP> G{mem}, Q{mem + SZ}, P{mem + 2 * SZ}, T{mem + 3 * SZ};
+  const int ri = muon_find(p, blockIdx.x, true);
+  const MuonRun& r = p.run[ri];
+  const int mat = blockIdx.x - r.mat0, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool wide = r.rows <= r.cols;
+  // G, at the matrix's own indices (a tall matrix's fragment f holds columns
+  // F c + f).
+  const f64x4* in = reinterpret_cast<const f64x4*>(p.part) +
+                    ((int64_t)r.blk0 + (int64_t)mat * r.splits) * NT * 64;
+  for (int i = wave; i < NT; i += 4) {
+    f64x4 s = in[i * 64 + lane];
+    for (int q = 1; q < r.splits; ++q) s += in[((int64_t)q * NT + i) * 64 + lane];
+    int t, u;
+    muon_tile<RP>(i, t, u);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int rc = 4 * v + (lane >> 4), cc = lane & 15;
+      const int row = wide ? 16 * t + rc : F * rc + t, col = wide ? 16 * u + cc : F * cc + u;
+      G.at(row, col) = s[v];
+      G.at(col, row) = s[v];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < RP) diag[threadIdx.x] = G.at(threadIdx.x, threadIdx.x);
+  __syncthreads();
+  double tr = 0.0;
+  for (int i = 0; i < RP; ++i) tr += diag[i];
+  const double norm = sqrt(tr) + p.eps;
+  const double inv = norm > 0.0 || norm != norm ? 1.0 / norm : 0.0;   // a NaN stays one
+  for (int i = threadIdx.x; i < RP * RP; i += 256) G.at(i / RP, i % RP) *= inv * inv;
+  __syncthreads();
+  for (int k = 0; k < p.steps; ++k) {
+    // Q = a I + b G + c G^2 (the first step's P, too)
+    for (int i = wave; i < NT; i += 4) {
+      f64x4 d = sym_tile<RP>(G, G, i, lane);
+      int t, u;
+      muon_tile<RP>(i, t, u);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int row = 16 * t + 4 * v + (lane >> 4), col = 16 * u + (lane & 15);
+        d[v] = p.c * d[v] + p.b * G.at(row, col) + (row == col ? p.a : 0.0);
+      }
+      sym_store<RP>(Q, i, d, lane);
+      if (k == 0) sym_store<RP>(P, i, d, lane);
+    }
+    __syncthreads();
+    const bool last = k + 1 == p.steps;
+    f64x4 d[PER];
+    if (k > 0) {
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if (wave + 4 * q < NT) d[q] = sym_tile<RP>(Q, P, wave + 4 * q, lane);
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if (wave + 4 * q < NT) sym_store<RP>(P, wave + 4 * q, d[q], lane);
+    }
+    if (!last) {   // G <- Q (Q G)
+      for (int i = wave; i < NT; i += 4) sym_store<RP>(T, i, sym_tile<RP>(Q, G, i, lane), lane);
+      __syncthreads();
+      for (int i = wave; i < NT; i += 4) sym_store<RP>(G, i, sym_tile<RP>(Q, T, i, lane), lane);
+    }
+    __syncthreads();
+  }
+  double* out = p.poly + (int64_t)blockIdx.x * RP * RP;
+  for (int i = threadIdx.x; i < RP * RP; i += 256) out[i] = P.at(i / RP, i % RP) * inv;
+}
+
+// ------------------------------------------------------------------ apply
+// One wave's share: E groups of 16 long-side indices times P, or at RP 128
+// times one half of P's rows (the waves pair up, each with half the result).
+template <int RP, bool WIDE, bool VEC, bool MUON>
+LORA_DEV void apply_range(const MuonArgs& p, const MuonRun& r, const double* P, int64_t base, int k0,
+                          int k1, float sc) {
+  constexpr int F = RP / 16, E = RP >= 64 ? 2 : 4, LDP = RP + 4, NP = muon_parts<RP>(), FP = F / NP;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, h = lane >> 4;
+  const int t0 = (wave % NP) * FP;
+  for (int k = k0 + (wave / NP) * 16 * E; k < k1; k += (4 / NP) * 16 * E) {
+    f64x4 acc[FP][E];
+#pragma unroll
+    for (int t = 0; t < FP; ++t)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[t][e] = f64x4{0, 0, 0, 0};
+    auto u4 = [&](float* v, uint32_t at, int n, auto N_) {
+      constexpr int N = decltype(N_)::value;
+      ldn<VEC, N>(v, p.G + base, at, n);
+      if constexpr (MUON) {
+        float m[N];
+        ldn<VEC, N>(m, p.M + base, at, n);
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[q] = muon_u(p, v[q] * sc, m[q]);
+      }
+    };
+    if constexpr (WIDE) {
+      // Lane: row 4 s + h, columns k + E c .. of X; P's rows i = 16 t + c.
+      const int col = k + E * c;
+      const int n = col < k1 ? min(E, k1 - col) : 0;
+      float x[RP / 4][E];
+#pragma unroll
+      for (int s = 0; s < RP / 4; ++s) {
+        const int row = 4 * s + h;
+        u4(x[s], (uint32_t)row * (uint32_t)r.cols + (uint32_t)col, row < r.rows ? n : 0,
+           std::integral_constant<int, E>{});
+      }
+#pragma unroll
+      for (int s = 0; s < RP / 4; ++s) {
+#pragma unroll
+        for (int t = 0; t < FP; ++t) {
+          const double a = P[(16 * (t0 + t) + c) * LDP + 4 * s + h];
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[t][e] = mfma16x16x4_f64(a, (double)x[s][e], acc[t][e]);
+        }
+        // Keeps the reads of P from all being hoisted to the top (RP^2 / 64
+        // doubles a lane).
+        if (s % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int t = 0; t < FP; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int row = 16 * (t0 + t) + 4 * v + h;
+          const uint32_t at = (uint32_t)row * (uint32_t)r.cols + (uint32_t)col;
+          const int m = row < r.rows ? n : 0;
+          float o[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = (float)acc[t][e][v];
+          if constexpr (MUON) {
+            float w[E];
+            ldn<VEC, E>(w, p.P + base, at, m);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = w[e] - r.rate * o[e] - r.decay * w[e];
+          }
+          stn<VEC, E>(o, p.P + base, at, m);
+        }
+    } else {
+      // Lane: row k + 16 e + c of X, columns 16 s + 4 h ..; P's rows permuted
+      // so that a lane's four results are neighbours.
+      float x[E][F][4];
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int s = 0; s < F; ++s) {
+          const int row = k + 16 * e + c;
+          const int col = 16 * s + 4 * h;
+          u4(x[e][s], (uint32_t)row * (uint32_t)r.cols + (uint32_t)col, row < k1 && col < r.cols ? min(4, r.cols - col) : 0,
+             std::integral_constant<int, 4>{});
+        }
+      const int j = 4 * (c & 3) + (c >> 2);
+#pragma unroll
+      for (int s = 0; s < F; ++s) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int t = 0; t < FP; ++t) {
+            const double a = P[(16 * (t0 + t) + j) * LDP + 16 * s + 4 * h + q];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              acc[t][e] = mfma16x16x4_f64(a, (double)x[e][s][q], acc[t][e]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int t = 0; t < FP; ++t) {
+          const int row = k + 16 * e + c;
+          const int col = 16 * (t0 + t) + 4 * h;
+          const uint32_t at = (uint32_t)row * (uint32_t)r.cols + (uint32_t)col;
+          const int m = row < k1 && col < r.cols ? min(4, r.cols - col) : 0;
+          float o[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) o[v] = (float)acc[t][e][v];
+          if constexpr (MUON) {
+            float w[4];
+            ldn<VEC, 4>(w, p.P + base, at, m);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) o[v] = w[v] - r.rate * o[v] - r.decay * w[v];
+          }
+          stn<VEC, 4>(o, p.P + base, at, m);
+        }
+    }
+  }
+}
+
+template <int RP, bool VEC, bool MUON>
+__global__ __launch_bounds__(256, RP == 128 ? 1 : 2) void muon_apply_kernel(MuonArgs p) {
+  constexpr int LDP = RP + 4;
+  __shared__ double P[RP * LDP];
+  if (muon_vetoed(p)) return;
+  const float sc = p.d_scale ? *p.d_scale : 1.0f;
+  const int ri = muon_find(p, blockIdx.x, false);
+  const MuonRun& r = p.run[ri];
+  const int rel = blockIdx.x - r.blk0, mat = rel / r.splits, sp = rel % r.splits;
+  const double* src = p.poly + (int64_t)(r.mat0 + mat) * RP * RP;
+  for (int i = threadIdx.x; i < RP * RP; i += 256) P[(i / RP) * LDP + i % RP] = src[i];
+  __syncthreads();
+  const bool wide = r.rows <= r.cols;
+  const int k0 = sp * r.len, k1 = min(wide ? r.cols : r.rows, k0 + r.len);
+  const int64_t base = r.offset + mat * r.stride;
+  if (wide) apply_range<RP, true, VEC, MUON>(p, r, P, base, k0, k1, sc);
+  else apply_range<RP, false, VEC, MUON>(p, r, P, base, k0, k1, sc);
+}
+
+}  // namespace lora

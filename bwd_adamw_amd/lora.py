@@ -27,7 +27,8 @@ __all__ = [
     "lora_qweight_layout", "lora_grad_prepare_noalloc",
     "lora_dora_row_norms_batch_workspace_bytes", "lora_dora_row_norms_batch", "QWeight", "qweight_pack", "Q_FORMATS", "EXPORTS", "GroupCall",
     "LoraNorm", "make_norm", "lora_norm_forward", "lora_norm_workspace_bytes",
-    "lora_norm_backward",
+    "lora_norm_backward", "LoraMatrixRun", "LoraMuonHparams", "make_matrix_run", "make_muon",
+    "lora_muon_workspace_bytes", "lora_orthogonalize", "lora_muon_step",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblora.so")
@@ -51,6 +52,7 @@ EXPORTS = (
     "lora_qweight_layout", "lora_grad_prepare_noalloc",
     "lora_dora_row_norms_batch_workspace_bytes", "lora_dora_row_norms_batch",
     "lora_norm_forward", "lora_norm_workspace_bytes", "lora_norm_backward",
+    "lora_muon_workspace_bytes", "lora_orthogonalize", "lora_muon_step",
 )
 
 
@@ -94,6 +96,18 @@ class LoraNorm(C.Structure):
                 ("beta", C.c_void_p), ("eps", C.c_float)]
 
 
+class LoraMatrixRun(C.Structure):
+    _fields_ = [("offset", C.c_int64), ("stride", C.c_int64), ("count", C.c_int64),
+                ("rows", C.c_int64), ("cols", C.c_int64), ("kind", C.c_int32)]
+
+
+class LoraMuonHparams(C.Structure):
+    _fields_ = [("lr", C.c_double), ("momentum", C.c_double), ("weight_decay", C.c_double),
+                ("plus_ratio", C.c_double), ("eps", C.c_double), ("a", C.c_double),
+                ("b", C.c_double), ("c", C.c_double), ("steps", C.c_int32),
+                ("nesterov", C.c_int32), ("adjust", C.c_int32)]
+
+
 _LIB = None
 
 
@@ -133,6 +147,9 @@ def lib() -> C.CDLL:
             "lora_qweight_layout": (SZ, [I32, I64, I64, P]),
             "lora_dora_row_norms_batch_workspace_bytes": (SZ, [I32, P]),
             "lora_dora_row_norms_batch": (I32, [I32, P, P, P, SZ, P]),
+            "lora_muon_workspace_bytes": (SZ, [P, I32]),
+            "lora_orthogonalize": (I32, [P, P, P, I32, P, P, SZ, P]),
+            "lora_muon_step": (I32, [P, P, P, P, I32, P, P, P, SZ, P]),
             "lora_norm_forward": (I32, [P, P, P, P, P]),
             "lora_norm_workspace_bytes": (SZ, [P]),
             "lora_norm_backward": (I32, [P, P, I32, P, P, P, P, P, I32, P, SZ, P]),
@@ -581,6 +598,70 @@ def lora_merge(lin: LoraLinear, W_out, rmse=None, ws=None, stream=None):
                           _sized(rmse, "rmse", 1, torch.float64), _ptr(ws, "ws", None), ws_bytes,
                           _stream(stream))
     _check("lora_merge", rc)
+
+
+# ------------------------------------------------------ orthogonalised update
+MUON_ADJUST = {"shape": 0, "rms": 1}
+
+
+def make_matrix_run(offset, rows, cols, count=1, stride=None, kind=KIND_A) -> LoraMatrixRun:
+    """`count` matrices [rows, cols] of an arena, the first at element
+    `offset`, `stride` elements apart (default: one after another)."""
+    return LoraMatrixRun(int(offset), int(rows * cols if stride is None else stride), int(count),
+                         int(rows), int(cols), int(kind))
+
+
+def make_muon(lr, momentum=0.95, weight_decay=0.0, plus_ratio=1.0, eps=1e-7,
+              coeffs=(3.4445, -4.7750, 2.0315), steps=5, nesterov=True,
+              adjust="shape") -> LoraMuonHparams:
+    """Hyper-parameters of lora_muon_step (and, without the step itself, of
+    lora_orthogonalize)."""
+    if adjust not in MUON_ADJUST:
+        raise ValueError(f"adjust must be one of {sorted(MUON_ADJUST)}, got {adjust!r}")
+    a, b, c = coeffs
+    return LoraMuonHparams(float(lr), float(momentum), float(weight_decay), float(plus_ratio),
+                           float(eps), float(a), float(b), float(c), int(steps),
+                           1 if nesterov else 0, MUON_ADJUST[adjust])
+
+
+def _runs(runs):
+    """The marshalled runs and the arena length that they reach."""
+    end = max((r.offset + (r.count - 1) * r.stride + r.rows * r.cols for r in runs), default=0)
+    return (LoraMatrixRun * len(runs))(*runs), end
+
+
+def lora_muon_workspace_bytes(runs) -> int:
+    return int(lib().lora_muon_workspace_bytes(_runs(runs)[0], len(runs)))
+
+
+def _muon_ws(arr, n, ws, device):
+    if ws is None:
+        ws = torch.empty(max(16, int(lib().lora_muon_workspace_bytes(arr, n))), device=device,
+                         dtype=torch.uint8)
+    return ws
+
+
+def lora_orthogonalize(G, O, runs, hp: LoraMuonHparams, ws=None, stream=None):
+    """O = the orthogonalised matrices of the arena G; `ws` is
+    taken from torch's allocator when None."""
+    arr, end = _runs(runs)
+    g, o = _sized(G, "G", end), _sized(O, "O", end)
+    ws = _muon_ws(arr, len(runs), ws, G.device)
+    rc = lib().lora_orthogonalize(g, o, arr, len(runs), C.byref(hp), _ptr(ws, "ws", None),
+                                  ws.numel() * ws.element_size(), _stream(stream))
+    _check("lora_orthogonalize", rc)
+
+
+def lora_muon_step(params, grads, m, runs, hp: LoraMuonHparams, d_scale, ws=None, stream=None):
+    """Momentum, orthogonalisation and update of the matrices of `runs`;
+    `ws` is taken from torch's allocator when None."""
+    arr, end = _runs(runs)
+    p, g, mo = _sized(params, "params", end), _sized(grads, "grads", end), _sized(m, "m", end)
+    ws = _muon_ws(arr, len(runs), ws, params.device)
+    rc = lib().lora_muon_step(p, g, mo, arr, len(runs), C.byref(hp), _sized(d_scale, "d_scale", 1),
+                              _ptr(ws, "ws", None), ws.numel() * ws.element_size(),
+                              _stream(stream))
+    _check("lora_muon_step", rc)
 
 
 # --------------------------------------------------------------- row norms

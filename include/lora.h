@@ -356,6 +356,61 @@ size_t lora_merge_workspace_bytes(const lora_linear* lin);
 int lora_merge(const lora_linear* lin, void* W_out, int out_dtype, double* rmse, void* workspace,
                size_t workspace_bytes, void* stream);
 
+/* Orthogonalised update (Newton-Schulz): for each matrix u, with its short
+ * side R = min(rows, cols) <= 128 taken as rows,
+ *   X_0 = u / (||u||_F + eps),  X_{k+1} = (a I + b G + c G^2) X_k,
+ *   G = X_k X_k^T,  orth(u) = X_steps,
+ * which drives every singular value of u towards one.  Sums and the R x R
+ * polynomial are float64; the result is rounded once to float32.  A zero
+ * matrix gives zero.
+ *
+ * A run is `count` matrices of one shape, row-major in an arena, `stride`
+ * elements apart (the arenas of an adapter slot hold one run for each
+ * projection's A and one for each B).  Any sizes and offsets are accepted
+ * (LORA_E_SHAPE for a short side over 128 or a long one over 2^22); runs
+ * with cols, offset and stride multiples of 4 run faster.  The runs of one
+ * call must not overlap. */
+#define LORA_MAX_RUNS 32
+typedef struct lora_matrix_run {
+  int64_t offset, stride;   /* elements; stride is unused when count is 1  */
+  int64_t count, rows, cols;
+  int32_t kind;             /* 0 = LoRA A, 1 = LoRA B (see lora_segment)   */
+} lora_matrix_run;
+
+/* Size of a step: LORA_MUON_SHAPE lr * sqrt(max(1, rows / cols)),
+ * LORA_MUON_RMS lr * 0.2 * sqrt(max(rows, cols)) (the root mean square of an
+ * AdamW step). */
+typedef enum lora_muon_adjust {
+  LORA_MUON_SHAPE = 0,
+  LORA_MUON_RMS = 1
+} lora_muon_adjust;
+typedef struct lora_muon_hparams {
+  double lr, momentum, weight_decay, plus_ratio, eps;
+  double a, b, c;           /* coefficients of the quintic step            */
+  int32_t steps;            /* 1..10                                       */
+  int32_t nesterov;
+  int32_t adjust;           /* lora_muon_adjust                            */
+} lora_muon_hparams;
+
+size_t lora_muon_workspace_bytes(const lora_matrix_run* runs, int n);
+
+/* O = orth(G) for the matrices of `runs` (a host array of n runs, 1 to
+ * LORA_MAX_RUNS) in the arena G; of hp only eps, a, b, c and steps are used,
+ * but all of it has to be valid.  O must not overlap G. */
+int lora_orthogonalize(const float* G, float* O, const lora_matrix_run* runs, int n,
+                       const lora_muon_hparams* hp, void* ws, size_t ws_bytes, void* stream);
+
+/* One update of the matrices of `runs` (A and B; a slot's DoRA magnitudes
+ * stay with lora_adamw_step):
+ *   g' = grads * (*d_scale);  m = momentum m + g'
+ *   u = g' + momentum m (nesterov) or m
+ *   p -= rate orth(u);  A only: p -= lr weight_decay p_old
+ * rate = lr (B: lr plus_ratio) times the shape's factor.  When *d_scale is
+ * not finite (a vetoed update) nothing is changed. */
+int lora_muon_step(float* params, const float* grads, float* m, const lora_matrix_run* runs, int n,
+                   const lora_muon_hparams* hp, const float* d_scale, void* ws, size_t ws_bytes,
+                   void* stream);
+
 /* Row norms: the layer norm or RMS norm whose output is the X that a group of
  * adapted linears reads, over rows of X [rows, dim].  With mean_t the row's
  * mean (0 for RMS), rstd_t = 1 / sqrt(mean_k (x - mean_t)^2 + eps) and
