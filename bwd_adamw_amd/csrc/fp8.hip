@@ -1,0 +1,202 @@
+// Entry points of the 8-bit block-scaled products (include/lora.h:
+// lora_fp8_quantize, lora_fp8_product) and the plan of their launches.
+#include <string.h>
+
+#include <algorithm>
+
+#include "fp8.hpp"
+#include "host.hpp"
+#include "launch.hpp"
+
+using namespace lora;
+using namespace lora::host;
+
+namespace {
+
+// Tiles: tokens, columns, wave grid, stages in LDS (128, 128 and 60 KB of
+// them), blocks a CU holds, and the time of one contraction step of a CU's
+// resident blocks and of a block's ends, in microseconds.
+struct Fp8Cfg {
+  int bm, bn, per_cu;
+  double step, ends;
+};
+#define LORA_FP8_CFGS(X)                          \
+  X(0, 256, 256, 2, 4, 2, 1, 1.7, 6.0)            \
+  X(1, 128, 128, 2, 2, 2, 2, 1.1, 5.0)            \
+  X(2, 32, 128, 1, 4, 3, 2, 0.6, 4.0)
+constexpr Fp8Cfg kCfg[] = {
+#define LORA_FP8_ROW(i, bm, bn, wm, wn, ns, pc, st, en) {bm, bn, pc, st, en},
+    LORA_FP8_CFGS(LORA_FP8_ROW)
+#undef LORA_FP8_ROW
+};
+
+struct Fp8Plan {
+  int cfg, per, nsplit;
+};
+Fp8Plan plan(int64_t M, int64_t Nc, int nk) {
+  Fp8Plan best = {0, nk, 1};
+  double tb = 1e30;
+  for (int i = 0; i < 3; ++i) {
+    const Fp8Cfg& c = kCfg[i];
+    const int64_t tiles = cdiv(M, c.bm) * cdiv(Nc, c.bn);
+    for (int want = 1; want <= std::min(nk, 16); ++want) {
+      const int per = (int)cdiv(nk, want), n = (int)cdiv(nk, per);
+      if (n != want) continue;
+      const double rounds = (double)cdiv(tiles * n, kCUs * c.per_cu);
+      double t = rounds * (per * c.step + c.ends);
+      if (n > 1) t += 3.0 + 4.0 * M * Nc * (2.0 * n) / 4e6;
+      if (t < tb) {
+        tb = t;
+        best = {i, per, n};
+      }
+    }
+  }
+  return best;
+}
+
+template <bool DX, int OUT>
+void launch_gemm(int cfg, const Fp8Args& a, dim3 grid, hipStream_t st, const prof::Scope& ps) {
+#define LORA_FP8_LAUNCH(i, bm, bn, wm, wn, ns, pc, s_, e_) \
+  if (cfg == i)                                            \
+    return launch_n(fp8_gemm_kernel<bm, bn, wm, wn, ns, DX, OUT>, grid, 64u * wm * wn, st, ps, a);
+  LORA_FP8_CFGS(LORA_FP8_LAUNCH)
+#undef LORA_FP8_LAUNCH
+}
+
+int check_fp8(const lora_fp8_operand* x, int64_t N, int64_t K, int dx) {
+  if (!x) return LORA_E_INVALID;
+  if (x->rows <= 0 || x->cols <= 0 || N <= 0 || K <= 0) return LORA_E_SHAPE;
+  if (x->cols != (dx ? N : K)) return LORA_E_SHAPE;
+  if (!lora_fp8_weight_layout(N, K, nullptr) ||
+      !lora_fp8_operand_layout(x->rows, x->cols, nullptr))
+    return LORA_E_SHAPE;
+  return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_fp8_weight_layout(int64_t out_dim, int64_t in_dim, size_t* scale_offset) {
+  if (out_dim <= 0 || in_dim <= 0 || out_dim > (1 << 30) || in_dim > (1 << 30)) return 0;
+  const int64_t np = rup(out_dim, 128), kp = rup(in_dim, 128);
+  if (np * kp >= (1ll << 31)) return 0;
+  if (scale_offset) *scale_offset = (size_t)(np * kp);
+  return (size_t)(np * kp + (np / 128) * (kp / 128) * 4);
+}
+
+size_t lora_fp8_operand_layout(int64_t rows, int64_t cols, size_t* scale_offset) {
+  if (rows <= 0 || cols <= 0 || cols > (1 << 22) || rows > (1 << 30)) return 0;
+  // The exponents are addressed with 32-bit offsets.
+  if (rup(rows, 128) * cdiv(cols, 128) >= (1ll << 31)) return 0;
+  const size_t q = (size_t)(rows * rup(cols, 128));
+  const size_t off = (size_t)rup((int64_t)q, 256);
+  if (scale_offset) *scale_offset = off;
+  return off + (size_t)rup(rup(rows, 128) * cdiv(cols, 128), 256);
+}
+
+int lora_fp8_quantize(const void* X, int dtype, int64_t ldx, const lora_fp8_operand* out,
+                      void* stream) {
+  if (!out) return LORA_E_INVALID;
+  size_t off;
+  if (!lora_fp8_operand_layout(out->rows, out->cols, &off) || ldx < out->cols) return LORA_E_SHAPE;
+  if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_E_DTYPE;
+  if (!X || !out->data) return LORA_E_INVALID;
+  if (!al16(out->data) || ((uintptr_t)X & (dtype == LORA_F32 ? 3u : 1u))) return LORA_E_ALIGN;
+  Fp8QuantArgs a;
+  a.X = X;
+  a.Q = (uint8_t*)out->data;
+  a.E = a.Q + off;
+  a.rows = out->rows;
+  a.cols = out->cols;
+  a.ldx = ldx;
+  a.ldq = rup(out->cols, 128);
+  a.lde = rup(a.rows, 128);
+  const int64_t blocks = cdiv(a.rows * (a.ldq / 128), 16);
+  if (blocks > 0x7fffffffll) return LORA_E_SHAPE;
+  const int64_t unit = dtype == LORA_F32 ? 4 : 8;   // elements of a 16-byte load
+  const bool vec = al16(X) && ldx % unit == 0 && a.cols % unit == 0;
+  const double e = dtype == LORA_F32 ? 4.0 : 2.0;
+  prof::Scope ps("fp8_quant", a.rows, a.cols, 1, 3.0 * a.rows * a.cols, (e + 1.0) * a.rows * a.cols);
+  const dim3 grid((unsigned)blocks);
+  hipStream_t st = (hipStream_t)stream;
+  if (dtype == LORA_F32) {
+    if (vec) launch(fp8_quant_kernel<float, true>, grid, st, ps, a);
+    else launch(fp8_quant_kernel<float, false>, grid, st, ps, a);
+  } else {
+    if (vec) launch(fp8_quant_kernel<uint16_t, true>, grid, st, ps, a);
+    else launch(fp8_quant_kernel<uint16_t, false>, grid, st, ps, a);
+  }
+  return hip_status();
+}
+
+size_t lora_fp8_product_workspace_bytes(const lora_fp8_operand* x, int64_t out_dim, int64_t in_dim,
+                                        int dx) {
+  if (check_fp8(x, out_dim, in_dim, dx) != LORA_OK) return 0;
+  const int64_t Nc = dx ? in_dim : out_dim;
+  const Fp8Plan g = plan(x->rows, Nc, (int)cdiv(x->cols, 128));
+  return g.nsplit > 1 ? sizeof(float) * (size_t)(g.nsplit * x->rows * Nc) : 0;
+}
+
+int lora_fp8_product(const lora_fp8_operand* x, const void* W, int64_t out_dim, int64_t in_dim,
+                     int dx, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_fp8(x, out_dim, in_dim, dx);
+  if (rc) return rc;
+  if (out_dtype != LORA_F32 && out_dtype != LORA_BF16) return LORA_E_DTYPE;
+  if (!x->data || !W || !out) return LORA_E_INVALID;
+  if (!al16(x->data) || !al16(W) || !al16(out)) return LORA_E_ALIGN;
+  Fp8Args a;
+  memset(&a, 0, sizeof(a));
+  size_t off;
+  lora_fp8_operand_layout(x->rows, x->cols, &off);
+  a.M = x->rows;
+  a.Nc = dx ? in_dim : out_dim;
+  a.nk = (int)cdiv(x->cols, 128);
+  const Fp8Plan g = plan(a.M, a.Nc, a.nk);
+  const size_t need = lora_fp8_product_workspace_bytes(x, out_dim, in_dim, dx);
+  if (need && (!ws || ws_bytes < need || !al16(ws))) return LORA_E_WORKSPACE;
+  a.Q = (const uint8_t*)x->data;
+  a.E = a.Q + off;
+  a.ldw = rup(in_dim, 128);
+  a.W = (const uint8_t*)W;
+  a.S = (const float*)(a.W + rup(out_dim, 128) * a.ldw);
+  a.lds_ = a.ldw / 128;
+  a.C = out;
+  a.part = (float*)ws;
+  a.ldq = (int64_t)a.nk * 128;
+  a.lde = rup(a.M, 128);
+  a.per = g.per;
+  a.nsplit = g.nsplit;
+  const Fp8Cfg& c = kCfg[g.cfg];
+  const int64_t blocks = cdiv(a.M, c.bm) * cdiv(a.Nc, c.bn) * g.nsplit;
+  if (blocks > 0x7fffffffll) return LORA_E_SHAPE;
+  const dim3 grid((unsigned)blocks);
+  hipStream_t st = (hipStream_t)stream;
+  const double eo = out_dtype == LORA_F32 ? 4.0 : 2.0;
+  {
+    prof::Scope ps(dx ? "fp8_gemm_dx" : "fp8_gemm_fwd", a.M, a.Nc, x->cols,
+                   2.0 * a.M * a.Nc * x->cols,
+                   (double)a.M * a.ldq + (double)out_dim * in_dim +
+                       (g.nsplit > 1 ? 4.0 * g.nsplit : eo) * a.M * a.Nc);
+    const int o = g.nsplit > 1 ? 2 : out_dtype == LORA_BF16 ? 1 : 0;
+    if (dx) {
+      if (o == 0) launch_gemm<true, 0>(g.cfg, a, grid, st, ps);
+      else if (o == 1) launch_gemm<true, 1>(g.cfg, a, grid, st, ps);
+      else launch_gemm<true, 2>(g.cfg, a, grid, st, ps);
+    } else {
+      if (o == 0) launch_gemm<false, 0>(g.cfg, a, grid, st, ps);
+      else if (o == 1) launch_gemm<false, 1>(g.cfg, a, grid, st, ps);
+      else launch_gemm<false, 2>(g.cfg, a, grid, st, ps);
+    }
+  }
+  if (g.nsplit > 1) {
+    const int64_t n = a.M * a.Nc;
+    prof::Scope ps("fp8_reduce", a.M, a.Nc, g.nsplit, 0.0, (4.0 * g.nsplit + eo) * n);
+    const dim3 rg((unsigned)cdiv(n, 1024));
+    if (out_dtype == LORA_BF16) launch(fp8_reduce_kernel<true>, rg, st, ps, (const float*)ws, n, g.nsplit, out);
+    else launch(fp8_reduce_kernel<false>, rg, st, ps, (const float*)ws, n, g.nsplit, out);
+  }
+  return hip_status();
+}
+
+}  // extern "C"

@@ -29,6 +29,9 @@ __all__ = [
     "LoraNorm", "make_norm", "lora_norm_forward", "lora_norm_workspace_bytes",
     "lora_norm_backward", "LoraMatrixRun", "LoraMuonHparams", "make_matrix_run", "make_muon",
     "lora_muon_workspace_bytes", "lora_orthogonalize", "lora_muon_step",
+    "Fp8Weight", "fp8_pack", "Fp8Rows", "fp8_rows", "lora_fp8_weight_layout",
+    "lora_fp8_operand_layout", "lora_fp8_quantize", "lora_fp8_product_workspace_bytes",
+    "lora_fp8_product",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblora.so")
@@ -53,6 +56,8 @@ EXPORTS = (
     "lora_dora_row_norms_batch_workspace_bytes", "lora_dora_row_norms_batch",
     "lora_norm_forward", "lora_norm_workspace_bytes", "lora_norm_backward",
     "lora_muon_workspace_bytes", "lora_orthogonalize", "lora_muon_step",
+    "lora_fp8_weight_layout", "lora_fp8_operand_layout", "lora_fp8_quantize",
+    "lora_fp8_product_workspace_bytes", "lora_fp8_product",
 )
 
 
@@ -94,6 +99,10 @@ class LoraNorm(C.Structure):
     _fields_ = [("rows", C.c_int64), ("dim", C.c_int64), ("ldx", C.c_int64), ("ldy", C.c_int64),
                 ("kind", C.c_int32), ("dtype", C.c_int32), ("gamma", C.c_void_p),
                 ("beta", C.c_void_p), ("eps", C.c_float)]
+
+
+class LoraFp8Operand(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("data", C.c_void_p)]
 
 
 class LoraMatrixRun(C.Structure):
@@ -147,6 +156,11 @@ def lib() -> C.CDLL:
             "lora_qweight_layout": (SZ, [I32, I64, I64, P]),
             "lora_dora_row_norms_batch_workspace_bytes": (SZ, [I32, P]),
             "lora_dora_row_norms_batch": (I32, [I32, P, P, P, SZ, P]),
+            "lora_fp8_weight_layout": (SZ, [I64, I64, P]),
+            "lora_fp8_operand_layout": (SZ, [I64, I64, P]),
+            "lora_fp8_quantize": (I32, [P, I32, I64, P, P]),
+            "lora_fp8_product_workspace_bytes": (SZ, [P, I64, I64, I32]),
+            "lora_fp8_product": (I32, [P, P, I64, I64, I32, P, I32, P, SZ, P]),
             "lora_muon_workspace_bytes": (SZ, [P, I32]),
             "lora_orthogonalize": (I32, [P, P, P, I32, P, P, SZ, P]),
             "lora_muon_step": (I32, [P, P, P, P, I32, P, P, P, SZ, P]),
@@ -598,6 +612,105 @@ def lora_merge(lin: LoraLinear, W_out, rmse=None, ws=None, stream=None):
                           _sized(rmse, "rmse", 1, torch.float64), _ptr(ws, "ws", None), ws_bytes,
                           _stream(stream))
     _check("lora_merge", rc)
+
+
+# ------------------------------------------------------------ 8-bit products
+def _fp8_layout(fn, what, rows, cols):
+    off = C.c_size_t()
+    total = int(getattr(lib(), fn)(int(rows), int(cols), C.byref(off)))
+    if total == 0:
+        raise ValueError(f"no 8-bit layout for {what} [{rows}, {cols}]")
+    return total, int(off.value)
+
+
+def lora_fp8_weight_layout(out_dim, in_dim):
+    """(bytes, offset of the scales) of an 8-bit W [out_dim, in_dim]."""
+    return _fp8_layout("lora_fp8_weight_layout", "a weight", out_dim, in_dim)
+
+
+def lora_fp8_operand_layout(rows, cols):
+    """(bytes, offset of the exponents) of 8-bit activations [rows, cols]."""
+    return _fp8_layout("lora_fp8_operand_layout", "activations", rows, cols)
+
+
+class Fp8Weight:
+    """An 8-bit W [out_dim, in_dim] in the library's layout (include/lora.h):
+    one uint8 device buffer, e4m3 values in whole 128 x 128 blocks, then the
+    blocks' float32 scales."""
+
+    def __init__(self, out_dim: int, in_dim: int, buf: torch.Tensor):
+        total, _ = lora_fp8_weight_layout(out_dim, in_dim)
+        _sized(buf, "an 8-bit W", total, torch.uint8)
+        self.out_dim, self.in_dim, self.buf = int(out_dim), int(in_dim), buf
+
+    @property
+    def shape(self):
+        return (self.out_dim, self.in_dim)
+
+
+def fp8_pack(values, scales, device="cuda") -> Fp8Weight:
+    """Lay out e4m3 values [N, K] (float8_e4m3fn) and block scales
+    [ceil(N/128), ceil(K/128)] in one device buffer."""
+    N, K = values.shape
+    nb, kb = -(-N // 128), -(-K // 128)
+    if values.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"values must be float8_e4m3fn, got {values.dtype}")
+    if tuple(scales.shape) != (nb, kb):
+        raise ValueError(f"scales must be [{nb}, {kb}], got {list(scales.shape)}")
+    total, off = lora_fp8_weight_layout(N, K)
+    buf = torch.zeros(total, dtype=torch.uint8, device=device)
+    buf[:nb * 128 * kb * 128].view(nb * 128, kb * 128)[:N, :K].copy_(values.view(torch.uint8))
+    buf[off:off + 4 * nb * kb].copy_(scales.float().contiguous().view(torch.uint8).flatten())
+    return Fp8Weight(N, K, buf)
+
+
+class Fp8Rows:
+    """8-bit activations [rows, cols] with a power-of-two scale for each
+    128-wide block of a row, as lora_fp8_quantize leaves them."""
+
+    def __init__(self, rows: int, cols: int, buf: torch.Tensor):
+        self.rows, self.cols, self.buf = int(rows), int(cols), buf
+        total, _ = lora_fp8_operand_layout(rows, cols)
+        self.desc = LoraFp8Operand(self.rows, self.cols,
+                                   _sized(buf, "8-bit activations", total, torch.uint8))
+
+
+def fp8_rows(rows, cols, device="cuda") -> Fp8Rows:
+    """Room for 8-bit activations [rows, cols], from torch's allocator."""
+    return Fp8Rows(rows, cols, torch.empty(lora_fp8_operand_layout(rows, cols)[0], device=device,
+                                           dtype=torch.uint8))
+
+
+def lora_fp8_quantize(X, out: Fp8Rows, stream=None):
+    """Round X [rows, cols] (float32 or bfloat16, rows any distance apart)
+    into `out`."""
+    ld = X.stride(0) if isinstance(X, torch.Tensor) and X.dim() == 2 and out.rows > 1 else out.cols
+    dt = _act(X.dtype)
+    rc = lib().lora_fp8_quantize(_rows_ptr(X, "X", out.rows, out.cols, ld, dt), dt, ld,
+                                 C.byref(out.desc), _stream(stream))
+    _check("lora_fp8_quantize", rc)
+
+
+def lora_fp8_product_workspace_bytes(x: Fp8Rows, W: Fp8Weight, dx=False) -> int:
+    return int(lib().lora_fp8_product_workspace_bytes(C.byref(x.desc), W.out_dim, W.in_dim,
+                                                      1 if dx else 0))
+
+
+def lora_fp8_product(x: Fp8Rows, W: Fp8Weight, out, dx=False, ws=None, stream=None):
+    """out = x W^T, or x W with dx (x the rounded X or dY); out is float32 or
+    bfloat16, `ws` is taken from torch's allocator when None."""
+    if x.cols != (W.out_dim if dx else W.in_dim):
+        raise ValueError(f"x has {x.cols} columns for W [{W.out_dim}, {W.in_dim}], dx={dx}")
+    if ws is None:
+        need = lora_fp8_product_workspace_bytes(x, W, dx)
+        if need:
+            ws = torch.empty(need, device=out.device, dtype=torch.uint8)
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    rc = lib().lora_fp8_product(C.byref(x.desc), W.buf.data_ptr(), W.out_dim, W.in_dim,
+                                1 if dx else 0,
+                                _sized(out, "out", x.rows * (W.in_dim if dx else W.out_dim), None),
+                                _act(out.dtype), _ptr(ws, "ws", None), ws_bytes, _stream(stream))
+    _check("lora_fp8_product", rc)
 
 
 # ------------------------------------------------------ orthogonalised update

@@ -356,6 +356,49 @@ size_t lora_merge_workspace_bytes(const lora_linear* lin);
 int lora_merge(const lora_linear* lin, void* W_out, int out_dtype, double* rmse, void* workspace,
                size_t workspace_bytes, void* stream);
 
+/* 8-bit frozen products with a scale for each block of 128 (the frozen W of
+ * an 8-bit checkpoint).
+ *
+ * W [out_dim, in_dim] lies in one buffer (lora_fp8_weight_layout): its e4m3
+ * values as rows of in_dim rounded up to 128 bytes, out_dim rounded up to 128
+ * of them, zero past the matrix; then at *scale_offset the float32 scales
+ * [ceil(out_dim/128), ceil(in_dim/128)]: w = scale * value.
+ *
+ * Activations [rows, cols] are rounded to the same element type with a
+ * power-of-two scale for each 128-wide block of a row: the smallest 2^e, at
+ * least 2^-127, with max |x| <= 448 2^e; value = x 2^-e rounded to nearest
+ * even (the scaling is exact, this is the only rounding).  They lie in one
+ * buffer (lora_fp8_operand_layout): rows of cols rounded up to 128 bytes,
+ * zero past cols, then at *scale_offset the biased exponents e + 127, for each
+ * 128-wide block those of the rows, rounded up to 128, row t's at
+ * t - t % 128 + 8 (t % 16) + (t / 16) % 8.  NaN and infinities become NaN.
+ *
+ * Sizes below 1 are refused, as are cols over 2^22, rows over 2^30, and a W
+ * buffer or exponents of 2^31 bytes or more (LORA_E_SHAPE). */
+typedef struct lora_fp8_operand {
+  int64_t rows, cols;
+  void* data;               /* lora_fp8_operand_layout(rows, cols) bytes   */
+} lora_fp8_operand;
+
+/* Buffer sizes in bytes (0 for refused sizes); scale_offset may be NULL. */
+size_t lora_fp8_weight_layout(int64_t out_dim, int64_t in_dim, size_t* scale_offset);
+size_t lora_fp8_operand_layout(int64_t rows, int64_t cols, size_t* scale_offset);
+
+/* Rounds X [rows, cols] of dtype LORA_F32 or LORA_BF16, rows ldx elements
+ * apart, into `out` (any element alignment; 16-byte aligned rows are faster). */
+int lora_fp8_quantize(const void* X, int dtype, int64_t ldx, const lora_fp8_operand* out,
+                      void* stream);
+
+/* dx == 0: out [rows, out_dim] = x W^T, x [rows, in_dim] the rounded X;
+ * dx != 0: out [rows, in_dim] = x W, x [rows, out_dim] the rounded dY.
+ * out has type out_dtype, LORA_F32 or LORA_BF16 (rounded once, to nearest
+ * even).  The products run on 8-bit MFMA: exact products, a block's 128 summed
+ * to within 2^-14 of the largest, blocks summed in float32. */
+size_t lora_fp8_product_workspace_bytes(const lora_fp8_operand* x, int64_t out_dim, int64_t in_dim,
+                                        int dx);
+int lora_fp8_product(const lora_fp8_operand* x, const void* W, int64_t out_dim, int64_t in_dim,
+                     int dx, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
 /* Orthogonalised update (Newton-Schulz): for each matrix u, with its short
  * side R = min(rows, cols) <= 128 taken as rows,
  *   X_0 = u / (||u||_F + eps),  X_{k+1} = (a I + b G + c G^2) X_k,
