@@ -27,7 +27,8 @@ struct Class {          // the runs of one padded short side
   int64_t blocks, mats;
   double elems, flops;
   bool vec;
-  size_t part, poly, scratch, bytes;
+  size_t part, poly, bytes;
+  bool small;
 };
 
 int check_runs(const lora_matrix_run* runs, int n) {
@@ -60,9 +61,15 @@ int check_hparams(const lora_muon_hparams* h) {
 // partial of G costs as much memory time as 20 to 40 indices do).
 constexpr int64_t kMuonBlocks = 2 * kCUs, kMuonMinLen = 256;
 
+// Short sides up to 32 with long sides up to this run whole in one block: one
+// CU's float64 MFMA takes 3.3 us for each 1024 of them (both products), which
+// from about here on costs more than the two launches saved.
+constexpr int64_t kMuonSmallLen = 512;
+
 bool plan_class(const lora_matrix_run* runs, int n, int rp, const lora_muon_hparams* h, Class& c) {
   memset(&c, 0, sizeof(c));
   c.vec = true;
+  c.small = rp <= 32;
   for (int i = 0; i < n; ++i)
     if (muon_rp(std::min(runs[i].rows, runs[i].cols)) == rp) c.mats += runs[i].count;
   if (!c.mats) return false;
@@ -91,6 +98,7 @@ bool plan_class(const lora_matrix_run* runs, int n, int rp, const lora_muon_hpar
       r.rate = (float)(h->lr * f * (s.kind == 1 ? h->plus_ratio : 1.0));
       r.decay = s.kind == 0 ? (float)(h->lr * h->weight_decay) : 0.0f;
     }
+    c.small = c.small && L <= kMuonSmallLen;
     c.elems += (double)s.count * s.rows * s.cols;
     c.flops += (double)s.count * s.rows * s.cols * R;
     c.vec = c.vec && s.cols % 4 == 0 && s.offset % 4 == 0 && (s.count == 1 || s.stride % 4 == 0);
@@ -101,15 +109,20 @@ bool plan_class(const lora_matrix_run* runs, int n, int rp, const lora_muon_hpar
   off += (size_t)rup(blk * tiles(rp) * 64 * 32, 256);
   c.poly = off;
   off += (size_t)rup(mat * rp * rp * 8, 256);
-  c.scratch = off;
-  if (rp == 128) off += (size_t)(mat * poly_doubles<128>() * 8);
   c.bytes = off;
   return true;
 }
 
 template <int RP, bool VEC, bool MUON>
-void launch_class(const Class& c, char* ws, hipStream_t st) {
+void launch_class(const Class& c, hipStream_t st) {
   const double e = 4.0 * c.elems, part = 32.0 * 64 * tiles(RP) * c.blocks;
+  if constexpr (RP <= 32) {
+    if (c.small) {
+      prof::Scope ps("muon_small", c.mats, RP, c.a.steps, 3.0 * c.flops, (MUON ? 5 : 2) * e);
+      launch_n(muon_small_kernel<RP, VEC, MUON>, dim3((unsigned)c.mats), 1024u, st, ps, c.a);
+      return;
+    }
+  }
   if constexpr (RP == 128 && MUON) {
     prof::Scope ps("muon_momentum", c.mats, RP, c.blocks, 0.0, 3 * e);
     launch(muon_momentum_kernel<VEC>, dim3((unsigned)c.blocks), st, ps, c.a);
@@ -119,20 +132,20 @@ void launch_class(const Class& c, char* ws, hipStream_t st) {
     launch(muon_gram_kernel<RP, VEC, MUON>, dim3((unsigned)c.blocks), st, ps, c.a);
   }
   {
-    prof::Scope ps("muon_poly", c.mats, RP, c.a.steps, 4.0 * c.a.steps * c.mats * RP * RP * RP,
+    prof::Scope ps("muon_poly", c.mats, RP, c.a.steps, 8.0 * c.a.steps * c.mats * RP * RP * RP,
                    part + 8.0 * c.mats * RP * RP);
-    launch(muon_poly_kernel<RP>, dim3((unsigned)c.mats), st, ps, c.a, (double*)(ws + c.scratch));
+    launch_n(muon_poly_kernel<RP>, dim3((unsigned)c.mats), 64u * poly_nw<RP>(), st, ps, c.a);
   }
   prof::Scope ps("muon_apply", c.mats, RP, c.blocks, 2.0 * c.flops,
                  (MUON ? 4 : 2) * e + 8.0 * c.blocks * RP * RP);
   launch(muon_apply_kernel<RP, VEC, MUON>, dim3((unsigned)c.blocks), st, ps, c.a);
 }
 template <bool MUON>
-void launch_rp(int rp, const Class& c, char* ws, hipStream_t st) {
+void launch_rp(int rp, const Class& c, hipStream_t st) {
 #define LORA_MUON_RP(RP_)                                       \
   if (rp == RP_) {                                              \
-    if (c.vec) launch_class<RP_, true, MUON>(c, ws, st);        \
-    else launch_class<RP_, false, MUON>(c, ws, st);             \
+    if (c.vec) launch_class<RP_, true, MUON>(c, st);            \
+    else launch_class<RP_, false, MUON>(c, st);                 \
   }
   LORA_MUON_RP(16) LORA_MUON_RP(32) LORA_MUON_RP(64) LORA_MUON_RP(128)
 #undef LORA_MUON_RP
@@ -159,8 +172,8 @@ int run_all(const lora_matrix_run* runs, int n, const lora_muon_hparams* h, cons
     c.a.a = h->a;
     c.a.b = h->b;
     c.a.c = h->c;
-    if (M) launch_rp<true>(rp, c, (char*)ws, (hipStream_t)stream);
-    else launch_rp<false>(rp, c, (char*)ws, (hipStream_t)stream);
+    if (M) launch_rp<true>(rp, c, (hipStream_t)stream);
+    else launch_rp<false>(rp, c, (hipStream_t)stream);
   }
   return hip_status();
 }

@@ -215,12 +215,12 @@ constexpr int muon_part_tiles() {
   return muon_tiles<RP>() / muon_parts<RP>();
 }
 
-// PART's tiles (i % parts == PART) over the chunks of wave kw.
-template <int RP, bool WIDE, bool VEC, bool MUON, int PART>
+// PART's tiles (i % parts == PART) over the chunks of wave kw of KW.
+template <int RP, bool WIDE, bool VEC, bool MUON, int PART, int KW>
 LORA_DEV void gram_range(const MuonArgs& p, const MuonRun& r, int64_t base, int k0, int k1, int kw,
                          float sc, f64x4 (&acc)[muon_part_tiles<RP>()]) {
   typedef GramChunk<RP, WIDE, VEC, MUON> Chunk;
-  constexpr int F = Chunk::F, NP = muon_parts<RP>(), KW = 4 / NP;
+  constexpr int F = Chunk::F, NP = muon_parts<RP>();
   const int lane = threadIdx.x & 63;
   Chunk cur;
   int k = k0 + kw * Chunk::LEN;
@@ -272,31 +272,25 @@ __global__ __launch_bounds__(256) void muon_momentum_kernel(MuonArgs p) {
   }
 }
 
-template <int RP, bool VEC, bool MUON>
-__global__ __launch_bounds__(256, RP == 128 ? 1 : 2) void muon_gram_kernel(MuonArgs p) {
-  constexpr int NT = muon_tiles<RP>(), NP = muon_parts<RP>(), NA = muon_part_tiles<RP>();
-  __shared__ f64x4 sum[NT * 64];
-  if (muon_vetoed(p)) return;
-  const float sc = p.d_scale ? *p.d_scale : 1.0f;
-  const int ri = muon_find(p, blockIdx.x, false);
-  const MuonRun& r = p.run[ri];
-  const int rel = blockIdx.x - r.blk0, mat = rel / r.splits, sp = rel % r.splits;
-  const bool wide = r.rows <= r.cols;
-  const int k0 = sp * r.len, k1 = min(wide ? r.cols : r.rows, k0 + r.len);
-  const int64_t base = r.offset + mat * r.stride;
+// The Gram matrix of one block's range of a matrix, its upper tiles in `sum`
+// (the waves' sums, in wave order).  W waves.
+template <int RP, bool VEC, bool MUON, int W>
+LORA_DEV void gram_block(const MuonArgs& p, const MuonRun& r, int64_t base, int k0, int k1, float sc,
+                         f64x4* sum) {
+  constexpr int NP = muon_parts<RP>(), NA = muon_part_tiles<RP>(), KW = W / NP;
   f64x4 acc[NA];
 #pragma unroll
   for (int i = 0; i < NA; ++i) acc[i] = f64x4{0, 0, 0, 0};
+  const bool wide = r.rows <= r.cols;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, part = wave % NP, kw = wave / NP;
   if (part == 0) {
-    if (wide) gram_range<RP, true, VEC, MUON, 0>(p, r, base, k0, k1, kw, sc, acc);
-    else gram_range<RP, false, VEC, MUON, 0>(p, r, base, k0, k1, kw, sc, acc);
+    if (wide) gram_range<RP, true, VEC, MUON, 0, KW>(p, r, base, k0, k1, kw, sc, acc);
+    else gram_range<RP, false, VEC, MUON, 0, KW>(p, r, base, k0, k1, kw, sc, acc);
   } else {
-    if (wide) gram_range<RP, true, VEC, MUON, NP - 1>(p, r, base, k0, k1, kw, sc, acc);
-    else gram_range<RP, false, VEC, MUON, NP - 1>(p, r, base, k0, k1, kw, sc, acc);
+    if (wide) gram_range<RP, true, VEC, MUON, NP - 1, KW>(p, r, base, k0, k1, kw, sc, acc);
+    else gram_range<RP, false, VEC, MUON, NP - 1, KW>(p, r, base, k0, k1, kw, sc, acc);
   }
-  // The waves' sums, in wave order.
-  for (int w = 0; w < 4 / NP; ++w) {
+  for (int w = 0; w < KW; ++w) {
     if (kw == w) {
 #pragma unroll
       for (int i = 0; i < NA; ++i) {
@@ -306,141 +300,257 @@ __global__ __launch_bounds__(256, RP == 128 ? 1 : 2) void muon_gram_kernel(MuonA
     }
     __syncthreads();
   }
+}
+
+template <int RP, bool VEC, bool MUON>
+__global__ __launch_bounds__(256, RP == 128 ? 1 : 2) void muon_gram_kernel(MuonArgs p) {
+  constexpr int NT = muon_tiles<RP>();
+  __shared__ f64x4 sum[NT * 64];
+  if (muon_vetoed(p)) return;
+  const float sc = p.d_scale ? *p.d_scale : 1.0f;
+  const MuonRun& r = p.run[muon_find(p, blockIdx.x, false)];
+  const int rel = blockIdx.x - r.blk0, mat = rel / r.splits, sp = rel % r.splits;
+  const int k0 = sp * r.len, k1 = min(max(r.rows, r.cols), k0 + r.len);
+  gram_block<RP, VEC, MUON, 4>(p, r, r.offset + mat * r.stride, k0, k1, sc, sum);
   f64x4* out = reinterpret_cast<f64x4*>(p.part) + (int64_t)blockIdx.x * NT * 64;
   for (int i = threadIdx.x; i < NT * 64; i += 256) out[i] = sum[i];
 }
 
 // ------------------------------------------------------------------- poly
-// Symmetric RP x RP matrices, rows LD apart.  The padding puts the 32 lanes
-// of a half wave (eight rows, four columns) in different LDS banks.
+// Symmetric RP x RP matrices as 16 x 16 tiles in the layout that the matrix
+// instruction leaves a result in: value v of lane l is element (4 v + l / 16,
+// l % 16).  That is also its B operand of step v, and, the matrix being
+// symmetric, tile (w, t) is the A operand of step v for tile (t, w): a product
+// of two such matrices needs no rearrangement, only 16-byte LDS reads.
+//
+// The iteration takes 4 products a step (G^2, Q P, Q G, Q (Q G); the first
+// and last step fewer), 17 in all for five steps, on one CU, and is bound by
+// its float64 MFMA (32 to 35 ns an instruction and SIMD, measured).  Up to
+// RP 64 all matrices are in LDS (128 KB at 64) and only the upper tiles are
+// computed, 5/8 of them at 64; stores mirror them.  RP 128 keeps one tile
+// column of each matrix in the registers of eight waves, only the left factor
+// in LDS (128 KB).
 template <int RP>
-struct Sym {
-  static constexpr int LD = RP + 4;
-  double* p;
-  LORA_DEV double& at(int i, int j) const { return p[i * LD + j]; }
+struct PolyLds {
+  static constexpr int F = RP / 16, NM = F == 1 || F == 8 ? 1 : 4;
+  f64x4 a[NM][F * F * 64];   // tile (w, t) at (w F + t) 64
+  double diag[RP];
 };
-
-// Upper tile i of A B (A, B symmetric and commuting, so the product is too).
+// Waves of poly_waves, and the barriers that they meet at.
 template <int RP>
-LORA_DEV f64x4 sym_tile(const Sym<RP>& A, const Sym<RP>& B, int i, int lane) {
-  int t, u;
-  muon_tile<RP>(i, t, u);
-  const int c = lane & 15, h = lane >> 4;
+constexpr int poly_nw() {
+  return RP == 16 ? 1 : RP == 32 ? 4 : 8;
+}
+template <int RP>
+LORA_DEV int poly_syncs(int steps) {
+  return RP == 16 ? 2 : RP == 128 ? 2 + 4 * steps : 1 + 3 * steps;
+}
+
+// Tile (t, u) of A B.
+template <int F>
+LORA_DEV f64x4 sym_tile(const f64x4* A, const f64x4* B, int t, int u, int lane) {
   f64x4 d = {0, 0, 0, 0};
-#pragma unroll 8
-  for (int s = 0; s < RP / 4; ++s)
-    d = mfma16x16x4_f64(A.at(16 * t + c, 4 * s + h), B.at(16 * u + c, 4 * s + h), d);
+#pragma unroll
+  for (int w = 0; w < F; ++w) {
+    const f64x4 x = A[(w * F + t) * 64 + lane], y = B[(w * F + u) * 64 + lane];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) d = mfma16x16x4_f64(x[s], y[s], d);
+  }
   return d;
 }
-template <int RP>
-LORA_DEV void sym_store(const Sym<RP>& C, int i, f64x4 d, int lane) {
-  int t, u;
-  muon_tile<RP>(i, t, u);
+template <int F>
+LORA_DEV void sym_store(f64x4* M, int t, int u, f64x4 d, int lane) {
+  M[(t * F + u) * 64 + lane] = d;
+  if (t == u) return;
+  const int c = lane & 15, h = lane >> 4;
+  double* m = reinterpret_cast<double*>(M + ((u * F + t) * 64 + (c & 3) * 16 + h)) + (c >> 2);
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int row = 16 * t + 4 * v + (lane >> 4), col = 16 * u + (lane & 15);
-    C.at(row, col) = d[v];
-    C.at(col, row) = d[v];
-  }
+  for (int v = 0; v < 4; ++v) m[16 * v] = d[v];
 }
 
-// LDS for RP <= 64 (four matrices, 139 KB at 64); device memory for 128,
-// whose four matrices (540 KB) stay in the block's L2.
-template <int RP>
-constexpr bool poly_lds() {
-  return RP <= 64;
-}
-template <int RP>
-constexpr int64_t poly_doubles() {
-  return 4 * (int64_t)RP * Sym<RP>::LD;
+// Column u of A B: A in LDS, or (F 1) its own tile; column u of B in registers.
+template <int F>
+LORA_DEV void col_mul(const f64x4* A, const f64x4 (&own)[F], const f64x4 (&B)[F], f64x4 (&C)[F],
+                      int lane) {
+#pragma unroll
+  for (int t = 0; t < F; ++t) C[t] = f64x4{0, 0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < F; ++w)
+#pragma unroll
+    for (int t = 0; t < F; ++t) {
+      const f64x4 x = F == 1 ? own[0] : A[(w * F + t) * 64 + lane];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) C[t] = mfma16x16x4_f64(x[s], B[w][s], C[t]);
+    }
 }
 
-template <int RP>
-__global__ __launch_bounds__(256) void muon_poly_kernel(MuonArgs p, double* scratch) {
-  constexpr int NT = muon_tiles<RP>(), F = RP / 16, PER = (NT + 3) / 4;
-  __shared__ double lds[poly_lds<RP>() ? poly_doubles<RP>() : 1];
-  __shared__ double diag[RP];
-  if (muon_vetoed(p)) return;
-  double* mem = poly_lds<RP>() ? lds : scratch + blockIdx.x * poly_doubles<RP>();
-  constexpr int64_t SZ = (int64_t)RP * Sym<RP>::LD;
-  const Sym<RP> G{mem}, Q{mem + SZ}, P{mem + 2 * SZ}, T{mem + 3 * SZ};
-  const int ri = muon_find(p, blockIdx.x, true);
-  const MuonRun& r = p.run[ri];
-  const int mat = blockIdx.x - r.mat0, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const bool wide = r.rows <= r.cols;
-  // G, at the matrix's own indices (a tall matrix's fragment f holds columns
-  // F c + f).
-  const f64x4* in = reinterpret_cast<const f64x4*>(p.part) +
-                    ((int64_t)r.blk0 + (int64_t)mat * r.splits) * NT * 64;
-  for (int i = wave; i < NT; i += 4) {
+// One matrix: G from the upper tiles in `in` (`splits` sets of them, added in
+// order), P / norm left in `out` [RP][RP], rows ldp apart.  Called by the
+// first poly_nw waves of a block; `sync` is the block's barrier.
+template <int RP, typename Sync>
+LORA_DEV void poly_waves(const MuonArgs& p, bool wide, const f64x4* in, int splits, PolyLds<RP>& m,
+                         double* out, int ldp, Sync sync) {
+  constexpr int F = RP / 16, NT = muon_tiles<RP>(), NW = poly_nw<RP>();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, h = lane >> 4;
+  double* const flat = reinterpret_cast<double*>(m.a[0]);
+  auto at = [&](int i, int j) -> double& {
+    return flat[(((i >> 4) * F + (j >> 4)) * 64 + (i & 3) * 16 + (j & 15)) * 4 + ((i >> 2) & 3)];
+  };
+  // A tall matrix's fragment f holds columns F c + f.
+  for (int i = wave; i < NT; i += NW) {
     f64x4 s = in[i * 64 + lane];
-    for (int q = 1; q < r.splits; ++q) s += in[((int64_t)q * NT + i) * 64 + lane];
-    int t, u;
-    muon_tile<RP>(i, t, u);
+#pragma unroll 4
+    for (int q = 1; q < splits; ++q) s += in[((int64_t)q * NT + i) * 64 + lane];
+    int t, w;
+    muon_tile<RP>(i, t, w);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int rc = 4 * v + (lane >> 4), cc = lane & 15;
-      const int row = wide ? 16 * t + rc : F * rc + t, col = wide ? 16 * u + cc : F * cc + u;
-      G.at(row, col) = s[v];
-      G.at(col, row) = s[v];
+      const int rc = 4 * v + h;
+      const int row = wide ? 16 * t + rc : F * rc + t, col = wide ? 16 * w + c : F * c + w;
+      at(row, col) = s[v];
+      at(col, row) = s[v];
     }
   }
-  __syncthreads();
-  if (threadIdx.x < RP) diag[threadIdx.x] = G.at(threadIdx.x, threadIdx.x);
-  __syncthreads();
+  sync();
+  for (int i = threadIdx.x; i < RP; i += 64 * NW) m.diag[i] = at(i, i);
+  sync();
   double tr = 0.0;
-  for (int i = 0; i < RP; ++i) tr += diag[i];
+#pragma unroll 16
+  for (int i = 0; i < RP; ++i) tr += m.diag[i];
   const double norm = sqrt(tr) + p.eps;
   const double inv = norm > 0.0 || norm != norm ? 1.0 / norm : 0.0;   // a NaN stays one
-  for (int i = threadIdx.x; i < RP * RP; i += 256) G.at(i / RP, i % RP) *= inv * inv;
-  __syncthreads();
-  for (int k = 0; k < p.steps; ++k) {
-    // Q = a I + b G + c G^2 (the first step's P, too)
-    for (int i = wave; i < NT; i += 4) {
-      f64x4 d = sym_tile<RP>(G, G, i, lane);
-      int t, u;
-      muon_tile<RP>(i, t, u);
+  // G is kept unscaled in LDS until the first step reads it.
+  const double inv2 = inv * inv;
+  auto poly = [&](f64x4 s, f64x4 g, bool diag) {   // a I + b G + c G^2
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      s[v] = p.c * s[v] + p.b * g[v] + (diag && 4 * v + h == c ? p.a : 0.0);
+    return s;
+  };
+
+  if constexpr (PolyLds<RP>::NM == 4) {
+    f64x4 *G = m.a[0], *Q = m.a[1], *P = m.a[2], *T = m.a[3];
+    constexpr int PER = (NT + NW - 1) / NW;
+    auto emit = [&](int t, int u, f64x4 d) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int row = 16 * t + 4 * v + (lane >> 4), col = 16 * u + (lane & 15);
-        d[v] = p.c * d[v] + p.b * G.at(row, col) + (row == col ? p.a : 0.0);
+        const int row = 16 * t + 4 * v + h, col = 16 * u + c;
+        out[row * ldp + col] = d[v] * inv;
+        out[col * ldp + row] = d[v] * inv;
       }
-      sym_store<RP>(Q, i, d, lane);
-      if (k == 0) sym_store<RP>(P, i, d, lane);
-    }
-    __syncthreads();
-    const bool last = k + 1 == p.steps;
-    f64x4 d[PER];
-    if (k > 0) {
+    };
+    for (int k = 0; k < p.steps; ++k) {
+      const bool last = k + 1 == p.steps;
+      // The first step's G is unscaled: G^2 takes inv2 twice.
+      const double g1 = k == 0 ? inv2 : 1.0, g2 = g1 * g1;
+      for (int i = wave; i < NT; i += NW) {
+        int t, u;
+        muon_tile<RP>(i, t, u);
+        const f64x4 d = poly(sym_tile<F>(G, G, t, u, lane) * g2, G[(t * F + u) * 64 + lane] * g1, t == u);
+        sym_store<F>(Q, t, u, d, lane);
+        if (k == 0) sym_store<F>(P, t, u, d, lane);
+        if (k == 0 && last) emit(t, u, d);
+      }
+      sync();
+      f64x4 d[PER];
 #pragma unroll
-      for (int q = 0; q < PER; ++q)
-        if (wave + 4 * q < NT) d[q] = sym_tile<RP>(Q, P, wave + 4 * q, lane);
-      __syncthreads();
+      for (int q = 0; q < PER; ++q) {
+        const int i = wave + NW * q;
+        if (k > 0 && i < NT) {
+          int t, u;
+          muon_tile<RP>(i, t, u);
+          d[q] = sym_tile<F>(Q, P, t, u, lane);
+          if (last) emit(t, u, d[q]);
+        }
+      }
+      if (last) {
+        sync();
+        break;
+      }
+      for (int i = NW - 1 - wave; i < NT; i += NW) {   // the other way round: waves share evenly
+        int t, u;
+        muon_tile<RP>(i, t, u);
+        sym_store<F>(T, t, u, sym_tile<F>(Q, G, t, u, lane) * g1, lane);
+      }
+      sync();
 #pragma unroll
-      for (int q = 0; q < PER; ++q)
-        if (wave + 4 * q < NT) sym_store<RP>(P, wave + 4 * q, d[q], lane);
+      for (int q = 0; q < PER; ++q) {
+        const int i = wave + NW * q;
+        if (k > 0 && i < NT) {
+          int t, u;
+          muon_tile<RP>(i, t, u);
+          sym_store<F>(P, t, u, d[q], lane);
+        }
+      }
+      for (int i = wave; i < NT; i += NW) {
+        int t, u;
+        muon_tile<RP>(i, t, u);
+        sym_store<F>(G, t, u, sym_tile<F>(Q, T, t, u, lane), lane);
+      }
+      sync();
     }
-    if (!last) {   // G <- Q (Q G)
-      for (int i = wave; i < NT; i += 4) sym_store<RP>(T, i, sym_tile<RP>(Q, G, i, lane), lane);
-      __syncthreads();
-      for (int i = wave; i < NT; i += 4) sym_store<RP>(G, i, sym_tile<RP>(Q, T, i, lane), lane);
+  } else {
+    f64x4* const A = m.a[0];
+    const int u = wave;
+    f64x4 G[F], Q[F], P[F], T[F];
+    auto put = [&](const f64x4(&M)[F]) {   // M becomes the left factor
+      if constexpr (F > 1) {
+        sync();
+#pragma unroll
+        for (int t = 0; t < F; ++t) A[(t * F + u) * 64 + lane] = M[t];
+        sync();
+      }
+    };
+#pragma unroll
+    for (int t = 0; t < F; ++t) G[t] = A[(t * F + u) * 64 + lane] * inv2;
+    for (int k = 0; k < p.steps; ++k) {
+      put(G);
+      col_mul<F>(A, G, G, Q, lane);
+#pragma unroll
+      for (int t = 0; t < F; ++t) Q[t] = poly(Q[t], G[t], t == u);
+      put(Q);
+      if (k == 0) {
+#pragma unroll
+        for (int t = 0; t < F; ++t) P[t] = Q[t];
+      } else {
+        col_mul<F>(A, Q, P, T, lane);
+#pragma unroll
+        for (int t = 0; t < F; ++t) P[t] = T[t];
+      }
+      if (k + 1 < p.steps) {
+        col_mul<F>(A, Q, G, T, lane);
+        col_mul<F>(A, Q, T, G, lane);
+      }
     }
-    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < F; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) out[(16 * t + 4 * v + h) * ldp + 16 * u + c] = P[t][v] * inv;
   }
-  double* out = p.poly + (int64_t)blockIdx.x * RP * RP;
-  for (int i = threadIdx.x; i < RP * RP; i += 256) out[i] = P.at(i / RP, i % RP) * inv;
+}
+
+template <int RP>
+__global__ __launch_bounds__(64 * poly_nw<RP>()) void muon_poly_kernel(MuonArgs p) {
+  __shared__ PolyLds<RP> m;
+  if (muon_vetoed(p)) return;
+  const MuonRun& r = p.run[muon_find(p, blockIdx.x, true)];
+  const int mat = blockIdx.x - r.mat0;
+  const f64x4* in = reinterpret_cast<const f64x4*>(p.part) +
+                    ((int64_t)r.blk0 + (int64_t)mat * r.splits) * muon_tiles<RP>() * 64;
+  poly_waves<RP>(p, r.rows <= r.cols, in, r.splits, m, p.poly + (int64_t)blockIdx.x * RP * RP, RP,
+                 [] { __syncthreads(); });
 }
 
 // ------------------------------------------------------------------ apply
 // One wave's share: E groups of 16 long-side indices times P, or at RP 128
 // times one half of P's rows (the waves pair up, each with half the result).
-template <int RP, bool WIDE, bool VEC, bool MUON>
+template <int RP, bool WIDE, bool VEC, bool MUON, int W>
 LORA_DEV void apply_range(const MuonArgs& p, const MuonRun& r, const double* P, int64_t base, int k0,
                           int k1, float sc) {
   constexpr int F = RP / 16, E = RP >= 64 ? 2 : 4, LDP = RP + 4, NP = muon_parts<RP>(), FP = F / NP;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, h = lane >> 4;
   const int t0 = (wave % NP) * FP;
-  for (int k = k0 + (wave / NP) * 16 * E; k < k1; k += (4 / NP) * 16 * E) {
+  for (int k = k0 + (wave / NP) * 16 * E; k < k1; k += (W / NP) * 16 * E) {
     f64x4 acc[FP][E];
 #pragma unroll
     for (int t = 0; t < FP; ++t)
@@ -553,17 +663,42 @@ __global__ __launch_bounds__(256, RP == 128 ? 1 : 2) void muon_apply_kernel(Muon
   __shared__ double P[RP * LDP];
   if (muon_vetoed(p)) return;
   const float sc = p.d_scale ? *p.d_scale : 1.0f;
-  const int ri = muon_find(p, blockIdx.x, false);
-  const MuonRun& r = p.run[ri];
+  const MuonRun& r = p.run[muon_find(p, blockIdx.x, false)];
   const int rel = blockIdx.x - r.blk0, mat = rel / r.splits, sp = rel % r.splits;
   const double* src = p.poly + (int64_t)(r.mat0 + mat) * RP * RP;
   for (int i = threadIdx.x; i < RP * RP; i += 256) P[(i / RP) * LDP + i % RP] = src[i];
   __syncthreads();
-  const bool wide = r.rows <= r.cols;
-  const int k0 = sp * r.len, k1 = min(wide ? r.cols : r.rows, k0 + r.len);
+  const int k0 = sp * r.len, k1 = min(max(r.rows, r.cols), k0 + r.len);
   const int64_t base = r.offset + mat * r.stride;
-  if (wide) apply_range<RP, true, VEC, MUON>(p, r, P, base, k0, k1, sc);
-  else apply_range<RP, false, VEC, MUON>(p, r, P, base, k0, k1, sc);
+  if (r.rows <= r.cols) apply_range<RP, true, VEC, MUON, 4>(p, r, P, base, k0, k1, sc);
+  else apply_range<RP, false, VEC, MUON, 4>(p, r, P, base, k0, k1, sc);
+}
+
+// All three steps of a small matrix in one block (sixteen waves): one launch
+// instead of three, with its second pass over the matrix in the CU's reach.
+template <int RP, bool VEC, bool MUON>
+__global__ __launch_bounds__(1024) void muon_small_kernel(MuonArgs p) {
+  constexpr int LDP = RP + 4, NT = muon_tiles<RP>();
+  __shared__ f64x4 sum[NT * 64];
+  __shared__ PolyLds<RP> m;
+  __shared__ double P[RP * LDP];
+  if (muon_vetoed(p)) return;
+  const float sc = p.d_scale ? *p.d_scale : 1.0f;
+  const MuonRun& r = p.run[muon_find(p, blockIdx.x, true)];
+  const int64_t base = r.offset + (int64_t)(blockIdx.x - r.mat0) * r.stride;
+  const int L = max(r.rows, r.cols);
+  const bool wide = r.rows <= r.cols;
+  gram_block<RP, VEC, MUON, 16>(p, r, base, 0, L, sc, sum);
+  // The first waves iterate; the others only join the barriers.
+  auto sync = [] { __syncthreads(); };
+  if ((int)threadIdx.x < 64 * poly_nw<RP>()) {
+    poly_waves<RP>(p, wide, sum, 1, m, P, LDP, sync);
+  } else {
+    for (int i = 0; i < poly_syncs<RP>(p.steps); ++i) sync();
+  }
+  __syncthreads();   // P, and the momentum that other waves wrote
+  if (wide) apply_range<RP, true, VEC, MUON, 16>(p, r, P, base, 0, L, sc);
+  else apply_range<RP, false, VEC, MUON, 16>(p, r, P, base, 0, L, sc);
 }
 
 }  // namespace lora

@@ -10,6 +10,7 @@ the call raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -200,8 +201,16 @@ def _sized(t, name, need, dtype=torch.float32):
     return p
 
 
+# The handle of the current stream.  torch.cuda.current_stream() builds a Stream
+# object on every call (2.8 us, as much as a launch); torch's own compiled code
+# asks for the bare handle (0.3 us with the device lookup).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -615,6 +624,7 @@ def lora_merge(lin: LoraLinear, W_out, rmse=None, ws=None, stream=None):
 
 
 # ------------------------------------------------------------ 8-bit products
+@functools.lru_cache(maxsize=256)   # a pure function of the sizes
 def _fp8_layout(fn, what, rows, cols):
     off = C.c_size_t()
     total = int(getattr(lib(), fn)(int(rows), int(cols), C.byref(off)))
