@@ -56,12 +56,14 @@ int check_hparams(const lora_muon_hparams* h) {
   return LORA_OK;
 }
 
-// Blocks: two of four waves a CU when there are matrices enough for it, each
-// over a range of whole 64-index tiles, at least 256 of them (a block's
-// partial of G costs as much memory time as 20 to 40 indices do).
-constexpr int64_t kMuonBlocks = 2 * kCUs, kMuonMinLen = 256;
+// Blocks: one round of what the CUs hold when there are matrices enough for
+// it, each over a range of whole 64-index tiles, at least two (more blocks
+// would shorten the other launches less than they lengthen the sums of their
+// partials: 36 x [64, 2560], 20 ranges instead of 14: 82 -> 90 us).
+int64_t muon_blocks(int rp) { return kCUs * (rp == 128 ? muon_per_cu<128>() : muon_per_cu<64>()); }
+constexpr int64_t kMuonMinLen = 128;
 
-// Short sides up to 32 with long sides up to this run whole in one block: one
+// Short sides up to 16 with long sides up to this run whole in one block: one
 // CU's float64 MFMA takes 3.3 us for each 1024 of them (both products), which
 // from about here on costs more than the two launches saved.
 constexpr int64_t kMuonSmallLen = 512;
@@ -69,11 +71,11 @@ constexpr int64_t kMuonSmallLen = 512;
 bool plan_class(const lora_matrix_run* runs, int n, int rp, const lora_muon_hparams* h, Class& c) {
   memset(&c, 0, sizeof(c));
   c.vec = true;
-  c.small = rp <= 32;
+  c.small = rp == 16;
   for (int i = 0; i < n; ++i)
     if (muon_rp(std::min(runs[i].rows, runs[i].cols)) == rp) c.mats += runs[i].count;
   if (!c.mats) return false;
-  const int64_t want = std::max<int64_t>(1, kMuonBlocks / c.mats);
+  const int64_t want = std::max<int64_t>(1, muon_blocks(rp) / c.mats);
   int64_t mat = 0, blk = 0;
   for (int i = 0; i < n; ++i) {
     const lora_matrix_run& s = runs[i];
@@ -116,7 +118,7 @@ bool plan_class(const lora_matrix_run* runs, int n, int rp, const lora_muon_hpar
 template <int RP, bool VEC, bool MUON>
 void launch_class(const Class& c, hipStream_t st) {
   const double e = 4.0 * c.elems, part = 32.0 * 64 * tiles(RP) * c.blocks;
-  if constexpr (RP <= 32) {
+  if constexpr (RP == 16) {
     if (c.small) {
       prof::Scope ps("muon_small", c.mats, RP, c.a.steps, 3.0 * c.flops, (MUON ? 5 : 2) * e);
       launch_n(muon_small_kernel<RP, VEC, MUON>, dim3((unsigned)c.mats), 1024u, st, ps, c.a);

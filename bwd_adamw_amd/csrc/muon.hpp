@@ -78,22 +78,31 @@ LORA_DEV bool muon_vetoed(const MuonArgs& p) {
 
 // N (1, 2 or 4) neighbouring values at element `at` of a matrix (under 2^30
 // elements: a scalar base and a 32-bit byte offset), of which the first n
-// exist.
+// exist; the others hold values of the matrix's first elements, for the caller
+// to mask when it uses them (maskn).  Every load is unconditional and nothing
+// looks at its result here: a guarded load becomes a branch, at whose end the
+// compiler waits for all loads in flight, and a select waits at once.
 template <bool VEC, int N>
 LORA_DEV void ldn(float* v, const float* base, uint32_t at, int n) {
-  const float* p = reinterpret_cast<const float*>(reinterpret_cast<const char*>(base) + 4u * at);
+  auto addr = [&](uint32_t i) {
+    return reinterpret_cast<const float*>(reinterpret_cast<const char*>(base) + 4u * i);
+  };
   if constexpr (VEC && N == 4) {
-    const f32x4 t = n > 0 ? *reinterpret_cast<const f32x4*>(p) : f32x4{0, 0, 0, 0};
+    const f32x4 t = *reinterpret_cast<const f32x4*>(addr(n > 0 ? at : 0));
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = t[e];
   } else if constexpr (VEC && N == 2) {
-    const f32x2 t = n > 0 ? *reinterpret_cast<const f32x2*>(p) : f32x2{0, 0};
+    const f32x2 t = *reinterpret_cast<const f32x2*>(addr(n > 0 ? at : 0));
     v[0] = t[0];
     v[1] = t[1];
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = e < n ? p[e] : 0.0f;
+    for (int e = 0; e < N; ++e) v[e] = *addr(e < n ? at + e : 0);
   }
+}
+template <bool VEC, int N>
+LORA_DEV float maskn(float v, int e, int n) {
+  return (VEC && N > 1 ? n > 0 : e < n) ? v : 0.0f;
 }
 template <bool VEC, int N>
 LORA_DEV void stn(const float* v, float* base, uint32_t at, int n) {
@@ -119,7 +128,7 @@ LORA_DEV float muon_u(const MuonArgs& p, float g, float m) {
 template <int RP, bool WIDE, bool VEC, bool MUON>
 struct GramChunk {
   static constexpr int F = RP / 16;
-  static constexpr int NK = RP >= 64 ? 4 : 8;   // 16 or 32 long-side indices
+  static constexpr int NK = RP >= 64 ? 4 : 8;   // 16 or 32 long-side indices, as registers allow
   static constexpr int LEN = 4 * NK;
   float g[F][NK], m[MUON ? F : 1][MUON ? NK : 1];
 
@@ -164,25 +173,23 @@ struct GramChunk {
     });
   }
   // The momentum's update (done before this kernel where waves share their
-  // chunks, RP 128); g becomes u.
+  // chunks, RP 128); g becomes u, zero where there is no element.
   LORA_DEV void update(const MuonArgs& p, const MuonRun& r, int64_t base, int k0, int k1, int lane,
                        float sc) {
-    if constexpr (MUON) {
+    each(r, k0, k1, lane, [&](int f, int s, uint32_t at, int n) {
+      float mv[Q];
 #pragma unroll
-      for (int f = 0; f < F; ++f)
-#pragma unroll
-        for (int s = 0; s < NK; ++s) {
-          const float gs = g[f][s] * sc;
-          if constexpr (RP < 128) m[f][s] = fmaf(p.mu, m[f][s], gs);
-          g[f][s] = muon_u(p, gs, m[f][s]);
+      for (int e = 0; e < Q; ++e) {
+        float& x = WIDE ? g[f][s + e] : g[f + e][s];
+        if constexpr (MUON) {
+          const float gs = x * sc, mo = WIDE ? m[f][s + e] : m[f + e][s];
+          mv[e] = RP < 128 ? fmaf(p.mu, mo, gs) : mo;
+          x = muon_u(p, gs, mv[e]);
         }
-      if constexpr (RP < 128) each(r, k0, k1, lane, [&](int f, int s, uint32_t at, int n) {
-        float v[Q];
-#pragma unroll
-        for (int e = 0; e < Q; ++e) v[e] = WIDE ? m[f][s + e] : m[f + e][s];
-        stn<VEC, Q>(v, p.M + base, at, n);
-      });
-    }
+        x = maskn<VEC, Q>(x, e, n);
+      }
+      if constexpr (MUON && RP < 128) stn<VEC, Q>(mv, p.M + base, at, n);
+    });
   }
 };
 
@@ -204,6 +211,12 @@ LORA_DEV void muon_tile(int i, int& t, int& u) {
   u = t + i;
 }
 
+// Blocks of four waves a CU, which their registers (and at 128 LDS) are held to.
+template <int RP>
+constexpr int muon_per_cu() {
+  return RP == 128 ? 1 : 2;
+}
+
 // Parts that the waves of a block split the result's tiles into: at RP 128
 // the 36 upper tiles (288 registers) are shared by two waves a chunk.
 template <int RP>
@@ -222,30 +235,36 @@ LORA_DEV void gram_range(const MuonArgs& p, const MuonRun& r, int64_t base, int 
   typedef GramChunk<RP, WIDE, VEC, MUON> Chunk;
   constexpr int F = Chunk::F, NP = muon_parts<RP>();
   const int lane = threadIdx.x & 63;
-  Chunk cur;
-  int k = k0 + kw * Chunk::LEN;
-  if (k >= k1) return;
-  cur.load(p, r, base, k, k1, lane);
-  for (;;) {
-    const int kn = k + KW * Chunk::LEN;
-    Chunk next;
-    if (kn < k1) next.load(p, r, base, kn, k1, lane);
-    cur.update(p, r, base, k, k1, lane, sc);
+  auto use = [&](Chunk& x, int k) {
+    x.update(p, r, base, k, k1, lane, sc);
 #pragma unroll
     for (int s = 0; s < Chunk::NK; ++s) {
-      double x[F];
+      double d[F];
 #pragma unroll
-      for (int f = 0; f < F; ++f) x[f] = (double)cur.g[f][s];
+      for (int f = 0; f < F; ++f) d[f] = (double)x.g[f][s];
       int i = 0;
 #pragma unroll
       for (int t = 0; t < F; ++t)
 #pragma unroll
         for (int u = t; u < F; ++u, ++i)
-          if (i % NP == PART) acc[i / NP] = mfma16x16x4_f64(x[t], x[u], acc[i / NP]);
+          if (i % NP == PART) acc[i / NP] = mfma16x16x4_f64(d[t], d[u], acc[i / NP]);
     }
-    if (kn >= k1) break;
-    k = kn;
-    cur = next;
+  };
+  // Two chunks take turns: one's loads are in flight while the other is used.
+  constexpr int STEP = KW * Chunk::LEN;
+  Chunk x, y;
+  int k = k0 + kw * Chunk::LEN;
+  if (k >= k1) return;
+  x.load(p, r, base, k, k1, lane);
+  for (;;) {
+    if (k + STEP < k1) y.load(p, r, base, k + STEP, k1, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    use(x, k);
+    if ((k += STEP) >= k1) break;
+    if (k + STEP < k1) x.load(p, r, base, k + STEP, k1, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    use(y, k);
+    if ((k += STEP) >= k1) break;
   }
 }
 
@@ -303,7 +322,7 @@ LORA_DEV void gram_block(const MuonArgs& p, const MuonRun& r, int64_t base, int 
 }
 
 template <int RP, bool VEC, bool MUON>
-__global__ __launch_bounds__(256, RP == 128 ? 1 : 2) void muon_gram_kernel(MuonArgs p) {
+__global__ __launch_bounds__(256, muon_per_cu<RP>()) void muon_gram_kernel(MuonArgs p) {
   constexpr int NT = muon_tiles<RP>();
   __shared__ f64x4 sum[NT * 64];
   if (muon_vetoed(p)) return;
@@ -327,13 +346,14 @@ __global__ __launch_bounds__(256, RP == 128 ? 1 : 2) void muon_gram_kernel(MuonA
 // and last step fewer), 17 in all for five steps, on one CU, and is bound by
 // its float64 MFMA (32 to 35 ns an instruction and SIMD, measured).  Up to
 // RP 64 all matrices are in LDS (128 KB at 64) and only the upper tiles are
-// computed, 5/8 of them at 64; stores mirror them.  RP 128 keeps one tile
-// column of each matrix in the registers of eight waves, only the left factor
-// in LDS (128 KB).
+// computed, 5/8 of them at 64; stores mirror them.  RP 128 has room for the
+// upper tiles of two matrices (144 KB): Q and the factor at hand, the others
+// in registers; reads of lower tiles transpose.
 template <int RP>
 struct PolyLds {
-  static constexpr int F = RP / 16, NM = F == 1 || F == 8 ? 1 : 4;
-  f64x4 a[NM][F * F * 64];   // tile (w, t) at (w F + t) 64
+  static constexpr int F = RP / 16, NM = F == 1 ? 1 : F == 8 ? 2 : 4;
+  // Tile (w, t) at (w F + t) 64; at F 8 the upper ones, one after another.
+  f64x4 a[NM][(F == 8 ? muon_tiles<RP>() : F * F) * 64];
   double diag[RP];
 };
 // Waves of poly_waves, and the barriers that they meet at.
@@ -343,7 +363,7 @@ constexpr int poly_nw() {
 }
 template <int RP>
 LORA_DEV int poly_syncs(int steps) {
-  return RP == 16 ? 2 : RP == 128 ? 2 + 4 * steps : 1 + 3 * steps;
+  return RP == 16 ? 2 : 1 + 3 * steps;   // not used at 128
 }
 
 // Tile (t, u) of A B.
@@ -368,22 +388,6 @@ LORA_DEV void sym_store(f64x4* M, int t, int u, f64x4 d, int lane) {
   for (int v = 0; v < 4; ++v) m[16 * v] = d[v];
 }
 
-// Column u of A B: A in LDS, or (F 1) its own tile; column u of B in registers.
-template <int F>
-LORA_DEV void col_mul(const f64x4* A, const f64x4 (&own)[F], const f64x4 (&B)[F], f64x4 (&C)[F],
-                      int lane) {
-#pragma unroll
-  for (int t = 0; t < F; ++t) C[t] = f64x4{0, 0, 0, 0};
-#pragma unroll
-  for (int w = 0; w < F; ++w)
-#pragma unroll
-    for (int t = 0; t < F; ++t) {
-      const f64x4 x = F == 1 ? own[0] : A[(w * F + t) * 64 + lane];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) C[t] = mfma16x16x4_f64(x[s], B[w][s], C[t]);
-    }
-}
-
 // One matrix: G from the upper tiles in `in` (`splits` sets of them, added in
 // order), P / norm left in `out` [RP][RP], rows ldp apart.  Called by the
 // first poly_nw waves of a block; `sync` is the block's barrier.
@@ -394,7 +398,9 @@ LORA_DEV void poly_waves(const MuonArgs& p, bool wide, const f64x4* in, int spli
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, h = lane >> 4;
   double* const flat = reinterpret_cast<double*>(m.a[0]);
   auto at = [&](int i, int j) -> double& {
-    return flat[(((i >> 4) * F + (j >> 4)) * 64 + (i & 3) * 16 + (j & 15)) * 4 + ((i >> 2) & 3)];
+    const int t = i >> 4, w = j >> 4;
+    const int tile = F == 8 ? t * F - t * (t - 1) / 2 + w - t : t * F + w;
+    return flat[(tile * 64 + (i & 3) * 16 + (j & 15)) * 4 + ((i >> 2) & 3)];
   };
   // A tall matrix's fragment f holds columns F c + f.
   for (int i = wave; i < NT; i += NW) {
@@ -407,8 +413,8 @@ LORA_DEV void poly_waves(const MuonArgs& p, bool wide, const f64x4* in, int spli
     for (int v = 0; v < 4; ++v) {
       const int rc = 4 * v + h;
       const int row = wide ? 16 * t + rc : F * rc + t, col = wide ? 16 * w + c : F * c + w;
-      at(row, col) = s[v];
-      at(col, row) = s[v];
+      if (F < 8 || (row >> 4) <= (col >> 4)) at(row, col) = s[v];
+      if (F < 8 || (col >> 4) <= (row >> 4)) at(col, row) = s[v];
     }
   }
   sync();
@@ -489,43 +495,87 @@ LORA_DEV void poly_waves(const MuonArgs& p, bool wide, const f64x4* in, int spli
       }
       sync();
     }
-  } else {
-    f64x4* const A = m.a[0];
-    const int u = wave;
-    f64x4 G[F], Q[F], P[F], T[F];
-    auto put = [&](const f64x4(&M)[F]) {   // M becomes the left factor
-      if constexpr (F > 1) {
-        sync();
+  } else if constexpr (F == 1) {
+    f64x4 G = m.a[0][lane] * inv2, P = G;
+    auto mul = [](f64x4 A, f64x4 B) {
+      f64x4 d = {0, 0, 0, 0};
 #pragma unroll
-        for (int t = 0; t < F; ++t) A[(t * F + u) * 64 + lane] = M[t];
-        sync();
-      }
+      for (int s = 0; s < 4; ++s) d = mfma16x16x4_f64(A[s], B[s], d);
+      return d;
     };
-#pragma unroll
-    for (int t = 0; t < F; ++t) G[t] = A[(t * F + u) * 64 + lane] * inv2;
     for (int k = 0; k < p.steps; ++k) {
-      put(G);
-      col_mul<F>(A, G, G, Q, lane);
-#pragma unroll
-      for (int t = 0; t < F; ++t) Q[t] = poly(Q[t], G[t], t == u);
-      put(Q);
-      if (k == 0) {
-#pragma unroll
-        for (int t = 0; t < F; ++t) P[t] = Q[t];
-      } else {
-        col_mul<F>(A, Q, P, T, lane);
-#pragma unroll
-        for (int t = 0; t < F; ++t) P[t] = T[t];
-      }
-      if (k + 1 < p.steps) {
-        col_mul<F>(A, Q, G, T, lane);
-        col_mul<F>(A, Q, T, G, lane);
-      }
+      const f64x4 Q = poly(mul(G, G), G, true);
+      P = k == 0 ? Q : mul(Q, P);
+      if (k + 1 < p.steps) G = mul(Q, mul(Q, G));
     }
 #pragma unroll
-    for (int t = 0; t < F; ++t)
+    for (int v = 0; v < 4; ++v) out[(4 * v + h) * ldp + c] = P[v] * inv;
+  } else {
+    // Q and one other matrix in LDS, by their upper tiles; a wave keeps its
+    // own tiles of the others.
+    f64x4 *A = m.a[0], *Q = m.a[1];
+    constexpr int PER = (NT + NW - 1) / NW;
+    auto tile = [&](const f64x4* M, int t, int u) {
+      if (t <= u) return M[(t * F - t * (t - 1) / 2 + u - t) * 64 + lane];
+      const double* q = reinterpret_cast<const double*>(
+                            M + (u * F - u * (u - 1) / 2 + t - u) * 64 + (c & 3) * 16 + h) + (c >> 2);
+      return f64x4{q[0], q[16], q[32], q[48]};
+    };
+    auto mul = [&](const f64x4* L, const f64x4* R, int t, int u) {
+      f64x4 d = {0, 0, 0, 0};
+#pragma unroll 2
+      for (int w = 0; w < F; ++w) {
+        const f64x4 x = tile(L, w, t), y = tile(R, w, u);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) out[(16 * t + 4 * v + h) * ldp + 16 * u + c] = P[t][v] * inv;
+        for (int s = 0; s < 4; ++s) d = mfma16x16x4_f64(x[s], y[s], d);
+      }
+      return d;
+    };
+    auto mine = [&](auto fn) {   // this wave's tiles
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const int i = wave + NW * q;
+        if (i < NT) {
+          int t, u;
+          muon_tile<RP>(i, t, u);
+          fn(q, i, t, u);
+        }
+      }
+    };
+    f64x4 P[PER], T[PER];
+    for (int k = 0; k < p.steps; ++k) {
+      const bool last = k + 1 == p.steps;
+      const double g1 = k == 0 ? inv2 : 1.0, g2 = g1 * g1;
+      mine([&](int q, int i, int t, int u) {
+        const f64x4 d = poly(mul(A, A, t, u) * g2, A[i * 64 + lane] * g1, t == u);
+        Q[i * 64 + lane] = d;
+        if (k == 0) P[q] = d;
+      });
+      sync();
+      if (!last) mine([&](int q, int, int t, int u) { T[q] = mul(Q, A, t, u) * g1; });
+      if (k > 0) {
+        sync();
+        mine([&](int q, int i, int, int) { A[i * 64 + lane] = P[q]; });
+        sync();
+        mine([&](int q, int, int t, int u) { P[q] = mul(Q, A, t, u); });
+      }
+      if (last) break;
+      sync();
+      mine([&](int q, int i, int, int) { A[i * 64 + lane] = T[q]; });
+      sync();
+      mine([&](int q, int, int t, int u) { T[q] = mul(Q, A, t, u); });
+      sync();
+      mine([&](int q, int i, int, int) { A[i * 64 + lane] = T[q]; });
+      sync();
+    }
+    mine([&](int q, int, int t, int u) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int row = 16 * t + 4 * v + h, col = 16 * u + c;
+        out[row * ldp + col] = P[q][v] * inv;
+        out[col * ldp + row] = P[q][v] * inv;
+      }
+    });
   }
 }
 
@@ -544,134 +594,133 @@ __global__ __launch_bounds__(64 * poly_nw<RP>()) void muon_poly_kernel(MuonArgs 
 // ------------------------------------------------------------------ apply
 // One wave's share: E groups of 16 long-side indices times P, or at RP 128
 // times one half of P's rows (the waves pair up, each with half the result).
-template <int RP, bool WIDE, bool VEC, bool MUON, int W>
+template <int RP, bool WIDE, bool VEC, bool MUON>
+struct ApplyChunk {
+  static constexpr int F = RP / 16, E = RP >= 64 ? 2 : 4;
+  static constexpr int NS = WIDE ? RP / 4 : E * F, N = WIDE ? E : 4;
+  float g[NS][N], m[MUON ? NS : 1][MUON ? N : 1];
+
+  // Access i.  Wide: row 4 i + h, E columns from k + E c.  Tall: row
+  // k + 16 (i / F) + c, four columns from 16 (i % F) + 4 h.
+  template <typename Fn>
+  LORA_DEV static void each(const MuonRun& r, int k, int k1, int lane, Fn fn) {
+    const int c = lane & 15, h = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int row = WIDE ? 4 * i + h : k + 16 * (i / F) + c;
+      const int col = WIDE ? k + E * c : 16 * (i % F) + 4 * h;
+      const bool in = WIDE ? row < r.rows && col < k1 : row < k1 && col < r.cols;
+      fn(i, (uint32_t)row * (uint32_t)r.cols + (uint32_t)col,
+         in ? min(N, (WIDE ? k1 : r.cols) - col) : 0);
+    }
+  }
+  LORA_DEV void load(const MuonArgs& p, const MuonRun& r, int64_t base, int k, int k1, int lane) {
+    each(r, k, k1, lane, [&](int i, uint32_t at, int n) {
+      ldn<VEC, N>(g[i], p.G + base, at, n);
+      if constexpr (MUON) ldn<VEC, N>(m[i], p.M + base, at, n);
+    });
+  }
+  LORA_DEV void to_u(const MuonArgs& p, const MuonRun& r, int k, int k1, int lane, float sc,
+                     float (&x)[NS][N]) {
+    each(r, k, k1, lane, [&](int i, uint32_t, int n) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        float u = g[i][e];
+        if constexpr (MUON) u = muon_u(p, u * sc, m[i][e]);
+        x[i][e] = maskn<VEC, N>(u, e, n);
+      }
+    });
+  }
+};
+
+// `ready` makes P ready (with a barrier) while the first chunk arrives.
+template <int RP, bool WIDE, bool VEC, bool MUON, int W, typename Ready>
 LORA_DEV void apply_range(const MuonArgs& p, const MuonRun& r, const double* P, int64_t base, int k0,
-                          int k1, float sc) {
-  constexpr int F = RP / 16, E = RP >= 64 ? 2 : 4, LDP = RP + 4, NP = muon_parts<RP>(), FP = F / NP;
+                          int k1, float sc, Ready ready) {
+  typedef ApplyChunk<RP, WIDE, VEC, MUON> Chunk;
+  constexpr int F = RP / 16, E = Chunk::E, LDP = RP + 4, NP = muon_parts<RP>(), FP = F / NP;
+  constexpr int NO = WIDE ? FP * 4 : E * FP, N = Chunk::N, STEP = (W / NP) * 16 * E;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, h = lane >> 4;
   const int t0 = (wave % NP) * FP;
-  for (int k = k0 + (wave / NP) * 16 * E; k < k1; k += (W / NP) * 16 * E) {
+  // Result i of a lane.  Wide: tile t0 + i / 4, row value i % 4, E columns.
+  // Tall: token group i / FP, tile t0 + i % FP, four columns.
+  auto results = [&](int k, auto fn) {
+#pragma unroll
+    for (int i = 0; i < NO; ++i) {
+      const int row = WIDE ? 16 * (t0 + i / 4) + 4 * (i % 4) + h : k + 16 * (i / FP) + c;
+      const int col = WIDE ? k + E * c : 16 * (t0 + i % FP) + 4 * h;
+      const bool in = WIDE ? row < r.rows && col < k1 : row < k1 && col < r.cols;
+      fn(i, (uint32_t)row * (uint32_t)r.cols + (uint32_t)col,
+         in ? min(N, (WIDE ? k1 : r.cols) - col) : 0);
+    }
+  };
+  int k = k0 + (wave / NP) * 16 * E;
+  Chunk q;
+  if (k < k1) q.load(p, r, base, k, k1, lane);
+  __builtin_amdgcn_sched_barrier(0);
+  ready();
+  for (; k < k1; k += STEP) {
+    float x[Chunk::NS][N], w[MUON ? NO : 1][MUON ? N : 1];
+    q.to_u(p, r, k, k1, lane, sc, x);
+    // This chunk's parameters and the next chunk arrive during the products.
+    if constexpr (MUON)
+      results(k, [&](int i, uint32_t at, int n) { ldn<VEC, N>(w[i], p.P + base, at, n); });
+    if (k + STEP < k1) q.load(p, r, base, k + STEP, k1, lane);
+    __builtin_amdgcn_sched_barrier(0);
     f64x4 acc[FP][E];
 #pragma unroll
     for (int t = 0; t < FP; ++t)
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[t][e] = f64x4{0, 0, 0, 0};
-    auto u4 = [&](float* v, uint32_t at, int n, auto N_) {
-      constexpr int N = decltype(N_)::value;
-      ldn<VEC, N>(v, p.G + base, at, n);
-      if constexpr (MUON) {
-        float m[N];
-        ldn<VEC, N>(m, p.M + base, at, n);
+    // Tall: P's rows permuted so that a lane's four results are neighbours.
+    const int j = WIDE ? c : 4 * (c & 3) + (c >> 2);
 #pragma unroll
-        for (int q = 0; q < N; ++q) v[q] = muon_u(p, v[q] * sc, m[q]);
-      }
-    };
-    if constexpr (WIDE) {
-      // Lane: row 4 s + h, columns k + E c .. of X; P's rows i = 16 t + c.
-      const int col = k + E * c;
-      const int n = col < k1 ? min(E, k1 - col) : 0;
-      float x[RP / 4][E];
+    for (int s = 0; s < RP / 4; ++s) {
 #pragma unroll
-      for (int s = 0; s < RP / 4; ++s) {
-        const int row = 4 * s + h;
-        u4(x[s], (uint32_t)row * (uint32_t)r.cols + (uint32_t)col, row < r.rows ? n : 0,
-           std::integral_constant<int, E>{});
-      }
+      for (int t = 0; t < FP; ++t) {
+        const double a = P[(16 * (t0 + t) + j) * LDP + (WIDE ? 4 * s + h : 16 * (s / 4) + 4 * h + s % 4)];
 #pragma unroll
-      for (int s = 0; s < RP / 4; ++s) {
-#pragma unroll
-        for (int t = 0; t < FP; ++t) {
-          const double a = P[(16 * (t0 + t) + c) * LDP + 4 * s + h];
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[t][e] = mfma16x16x4_f64(a, (double)x[s][e], acc[t][e]);
+        for (int e = 0; e < E; ++e) {
+          const double b = WIDE ? (double)x[s][e] : (double)x[e * F + s / 4][s % 4];
+          acc[t][e] = mfma16x16x4_f64(a, b, acc[t][e]);
         }
-        // Keeps the reads of P from all being hoisted to the top (RP^2 / 64
-        // doubles a lane).
-        if (s % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int t = 0; t < FP; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int row = 16 * (t0 + t) + 4 * v + h;
-          const uint32_t at = (uint32_t)row * (uint32_t)r.cols + (uint32_t)col;
-          const int m = row < r.rows ? n : 0;
-          float o[E];
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = (float)acc[t][e][v];
-          if constexpr (MUON) {
-            float w[E];
-            ldn<VEC, E>(w, p.P + base, at, m);
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = w[e] - r.rate * o[e] - r.decay * w[e];
-          }
-          stn<VEC, E>(o, p.P + base, at, m);
-        }
-    } else {
-      // Lane: row k + 16 e + c of X, columns 16 s + 4 h ..; P's rows permuted
-      // so that a lane's four results are neighbours.
-      float x[E][F][4];
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int s = 0; s < F; ++s) {
-          const int row = k + 16 * e + c;
-          const int col = 16 * s + 4 * h;
-          u4(x[e][s], (uint32_t)row * (uint32_t)r.cols + (uint32_t)col, row < k1 && col < r.cols ? min(4, r.cols - col) : 0,
-             std::integral_constant<int, 4>{});
-        }
-      const int j = 4 * (c & 3) + (c >> 2);
-#pragma unroll
-      for (int s = 0; s < F; ++s) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int t = 0; t < FP; ++t) {
-            const double a = P[(16 * (t0 + t) + j) * LDP + 16 * s + 4 * h + q];
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-              acc[t][e] = mfma16x16x4_f64(a, (double)x[e][s][q], acc[t][e]);
-          }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int t = 0; t < FP; ++t) {
-          const int row = k + 16 * e + c;
-          const int col = 16 * (t0 + t) + 4 * h;
-          const uint32_t at = (uint32_t)row * (uint32_t)r.cols + (uint32_t)col;
-          const int m = row < k1 && col < r.cols ? min(4, r.cols - col) : 0;
-          float o[4];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) o[v] = (float)acc[t][e][v];
-          if constexpr (MUON) {
-            float w[4];
-            ldn<VEC, 4>(w, p.P + base, at, m);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) o[v] = w[v] - r.rate * o[v] - r.decay * w[v];
-          }
-          stn<VEC, 4>(o, p.P + base, at, m);
-        }
+      // Keeps the reads of P from all being hoisted to the top (RP^2 / 64
+      // doubles a lane).
+      if (s % 4 == 3) __builtin_amdgcn_sched_barrier(0);
     }
+    results(k, [&](int i, uint32_t at, int n) {
+      float o[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        o[e] = (float)(WIDE ? acc[i / 4][e % E][i % 4] : acc[i % FP][i / FP][e]);
+        if constexpr (MUON) o[e] = w[i][e] - r.rate * o[e] - r.decay * w[i][e];
+      }
+      stn<VEC, N>(o, p.P + base, at, n);
+    });
   }
 }
 
 template <int RP, bool VEC, bool MUON>
-__global__ __launch_bounds__(256, RP == 128 ? 1 : 2) void muon_apply_kernel(MuonArgs p) {
+__global__ __launch_bounds__(256, muon_per_cu<RP>()) void muon_apply_kernel(MuonArgs p) {
   constexpr int LDP = RP + 4;
-  __shared__ double P[RP * LDP];
+  __shared__ __align__(16) double P[RP * LDP];
   if (muon_vetoed(p)) return;
   const float sc = p.d_scale ? *p.d_scale : 1.0f;
   const MuonRun& r = p.run[muon_find(p, blockIdx.x, false)];
   const int rel = blockIdx.x - r.blk0, mat = rel / r.splits, sp = rel % r.splits;
-  const double* src = p.poly + (int64_t)(r.mat0 + mat) * RP * RP;
-  for (int i = threadIdx.x; i < RP * RP; i += 256) P[(i / RP) * LDP + i % RP] = src[i];
-  __syncthreads();
+  typedef double f64x2 __attribute__((ext_vector_type(2)));
+  auto ready = [&] {
+    const f64x2* src = reinterpret_cast<const f64x2*>(p.poly + (int64_t)(r.mat0 + mat) * RP * RP);
+#pragma unroll
+    for (int i = 2 * threadIdx.x; i < RP * RP; i += 512)
+      *reinterpret_cast<f64x2*>(P + (i / RP) * LDP + i % RP) = src[i / 2];
+    __syncthreads();
+  };
   const int k0 = sp * r.len, k1 = min(max(r.rows, r.cols), k0 + r.len);
   const int64_t base = r.offset + mat * r.stride;
-  if (r.rows <= r.cols) apply_range<RP, true, VEC, MUON, 4>(p, r, P, base, k0, k1, sc);
-  else apply_range<RP, false, VEC, MUON, 4>(p, r, P, base, k0, k1, sc);
+  if (r.rows <= r.cols) apply_range<RP, true, VEC, MUON, 4>(p, r, P, base, k0, k1, sc, ready);
+  else apply_range<RP, false, VEC, MUON, 4>(p, r, P, base, k0, k1, sc, ready);
 }
 
 // All three steps of a small matrix in one block (sixteen waves): one launch
@@ -697,8 +746,8 @@ __global__ __launch_bounds__(1024) void muon_small_kernel(MuonArgs p) {
     for (int i = 0; i < poly_syncs<RP>(p.steps); ++i) sync();
   }
   __syncthreads();   // P, and the momentum that other waves wrote
-  if (wide) apply_range<RP, true, VEC, MUON, 16>(p, r, P, base, 0, L, sc);
-  else apply_range<RP, false, VEC, MUON, 16>(p, r, P, base, 0, L, sc);
+  if (wide) apply_range<RP, true, VEC, MUON, 16>(p, r, P, base, 0, L, sc, [] {});
+  else apply_range<RP, false, VEC, MUON, 16>(p, r, P, base, 0, L, sc, [] {});
 }
 
 }  // namespace lora
