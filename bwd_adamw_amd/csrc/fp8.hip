@@ -33,13 +33,14 @@ constexpr Fp8Cfg kCfg[] = {
 struct Fp8Plan {
   int cfg, per, nsplit;
 };
-Fp8Plan plan(int64_t M, int64_t Nc, int nk) {
+// most: the largest number of splits.
+Fp8Plan plan(int64_t M, int64_t Nc, int nk, int most = 16) {
   Fp8Plan best = {0, nk, 1};
   double tb = 1e30;
   for (int i = 0; i < 3; ++i) {
     const Fp8Cfg& c = kCfg[i];
     const int64_t tiles = cdiv(M, c.bm) * cdiv(Nc, c.bn);
-    for (int want = 1; want <= std::min(nk, 16); ++want) {
+    for (int want = 1; want <= std::min(nk, most); ++want) {
       const int per = (int)cdiv(nk, want), n = (int)cdiv(nk, per);
       if (n != want) continue;
       const double rounds = (double)cdiv(tiles * n, kCUs * c.per_cu);
@@ -73,7 +74,82 @@ int check_fp8(const lora_fp8_operand* x, int64_t N, int64_t K, int dx) {
   return LORA_OK;
 }
 
+// Everything but the output and the split of a product.
+Fp8Args product_args(const void* x, int64_t rows, const void* W, int64_t N, int64_t K, bool dx) {
+  Fp8Args a;
+  memset(&a, 0, sizeof(a));
+  a.M = rows;
+  a.Nc = dx ? K : N;
+  a.nk = (int)cdiv(dx ? N : K, 128);
+  a.ldq = (int64_t)a.nk * 128;
+  a.lde = rup(rows, 128);
+  a.Q = (const uint8_t*)x;
+  a.E = a.Q + rup(rows * a.ldq, 256);
+  a.ldw = rup(K, 128);
+  a.W = (const uint8_t*)W;
+  a.S = (const float*)(a.W + rup(N, 128) * a.ldw);
+  a.lds_ = a.ldw / 128;
+  return a;
+}
+
+void quantize(const void* X, int dtype, int64_t ldx, int64_t rows, int64_t cols, void* data,
+              hipStream_t st) {
+  Fp8QuantArgs a;
+  a.X = X;
+  a.Q = (uint8_t*)data;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.ldq = rup(cols, 128);
+  a.lde = rup(rows, 128);
+  a.E = a.Q + rup(rows * a.ldq, 256);
+  const int64_t unit = dtype == LORA_F32 ? 4 : 8;   // elements of a 16-byte load
+  const bool vec = al16(X) && ldx % unit == 0 && cols % unit == 0;
+  const double e = dtype == LORA_F32 ? 4.0 : 2.0;
+  prof::Scope ps("fp8_quant", rows, cols, 1, 3.0 * rows * cols, (e + 1.0) * rows * cols);
+  const dim3 grid((unsigned)cdiv(rows * (a.ldq / 128), 16));
+  if (dtype == LORA_F32) {
+    if (vec) launch(fp8_quant_kernel<float, true>, grid, st, ps, a);
+    else launch(fp8_quant_kernel<float, false>, grid, st, ps, a);
+  } else {
+    if (vec) launch(fp8_quant_kernel<uint16_t, true>, grid, st, ps, a);
+    else launch(fp8_quant_kernel<uint16_t, false>, grid, st, ps, a);
+  }
+}
+
 }  // namespace
+
+namespace lora {
+
+size_t fp8_operand_bytes(int64_t rows, int64_t cols) {
+  return lora_fp8_operand_layout(rows, cols, nullptr);
+}
+
+void fp8_launch_quantize(const float* X, int64_t rows, int64_t cols, void* data, hipStream_t st) {
+  quantize(X, LORA_F32, cols, rows, cols, data, st);
+}
+
+void fp8_launch_lora_product(const void* x, int64_t rows, const void* W, int64_t N, int64_t K,
+                             bool dx, const Fp8Lora& l, float* out, float* out2, hipStream_t st) {
+  Fp8Args a = product_args(x, rows, W, N, K, dx);
+  // One block sums the whole contraction: the LoRA term joins it there.
+  const Fp8Plan g = plan(a.M, a.Nc, a.nk, 1);
+  a.per = a.nk;
+  a.nsplit = 1;
+  a.C = out;
+  a.C2 = out2;
+  a.lora = l;
+  const Fp8Cfg& c = kCfg[g.cfg];
+  const int64_t Kc = dx ? N : K;
+  prof::Scope ps(dx ? "fp8_gemm_dx" : "fp8_gemm_fwd", a.M, a.Nc, Kc,
+                 2.0 * a.M * a.Nc * (Kc + l.r),
+                 (double)a.M * a.ldq + (double)N * K + 4.0 * a.M * a.Nc * (out2 ? 2 : 1));
+  const dim3 grid((unsigned)(cdiv(a.M, c.bm) * cdiv(a.Nc, c.bn)));
+  if (dx) launch_gemm<true, 3>(g.cfg, a, grid, st, ps);
+  else launch_gemm<false, 3>(g.cfg, a, grid, st, ps);
+}
+
+}  // namespace lora
 
 extern "C" {
 
@@ -98,35 +174,12 @@ size_t lora_fp8_operand_layout(int64_t rows, int64_t cols, size_t* scale_offset)
 int lora_fp8_quantize(const void* X, int dtype, int64_t ldx, const lora_fp8_operand* out,
                       void* stream) {
   if (!out) return LORA_E_INVALID;
-  size_t off;
-  if (!lora_fp8_operand_layout(out->rows, out->cols, &off) || ldx < out->cols) return LORA_E_SHAPE;
+  if (!lora_fp8_operand_layout(out->rows, out->cols, nullptr) || ldx < out->cols) return LORA_E_SHAPE;
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_E_DTYPE;
   if (!X || !out->data) return LORA_E_INVALID;
   if (!al16(out->data) || ((uintptr_t)X & (dtype == LORA_F32 ? 3u : 1u))) return LORA_E_ALIGN;
-  Fp8QuantArgs a;
-  a.X = X;
-  a.Q = (uint8_t*)out->data;
-  a.E = a.Q + off;
-  a.rows = out->rows;
-  a.cols = out->cols;
-  a.ldx = ldx;
-  a.ldq = rup(out->cols, 128);
-  a.lde = rup(a.rows, 128);
-  const int64_t blocks = cdiv(a.rows * (a.ldq / 128), 16);
-  if (blocks > 0x7fffffffll) return LORA_E_SHAPE;
-  const int64_t unit = dtype == LORA_F32 ? 4 : 8;   // elements of a 16-byte load
-  const bool vec = al16(X) && ldx % unit == 0 && a.cols % unit == 0;
-  const double e = dtype == LORA_F32 ? 4.0 : 2.0;
-  prof::Scope ps("fp8_quant", a.rows, a.cols, 1, 3.0 * a.rows * a.cols, (e + 1.0) * a.rows * a.cols);
-  const dim3 grid((unsigned)blocks);
-  hipStream_t st = (hipStream_t)stream;
-  if (dtype == LORA_F32) {
-    if (vec) launch(fp8_quant_kernel<float, true>, grid, st, ps, a);
-    else launch(fp8_quant_kernel<float, false>, grid, st, ps, a);
-  } else {
-    if (vec) launch(fp8_quant_kernel<uint16_t, true>, grid, st, ps, a);
-    else launch(fp8_quant_kernel<uint16_t, false>, grid, st, ps, a);
-  }
+  if (cdiv(out->rows * (rup(out->cols, 128) / 128), 16) > 0x7fffffffll) return LORA_E_SHAPE;
+  quantize(X, dtype, ldx, out->rows, out->cols, out->data, (hipStream_t)stream);
   return hip_status();
 }
 
@@ -145,26 +198,12 @@ int lora_fp8_product(const lora_fp8_operand* x, const void* W, int64_t out_dim, 
   if (out_dtype != LORA_F32 && out_dtype != LORA_BF16) return LORA_E_DTYPE;
   if (!x->data || !W || !out) return LORA_E_INVALID;
   if (!al16(x->data) || !al16(W) || !al16(out)) return LORA_E_ALIGN;
-  Fp8Args a;
-  memset(&a, 0, sizeof(a));
-  size_t off;
-  lora_fp8_operand_layout(x->rows, x->cols, &off);
-  a.M = x->rows;
-  a.Nc = dx ? in_dim : out_dim;
-  a.nk = (int)cdiv(x->cols, 128);
+  Fp8Args a = product_args(x->data, x->rows, W, out_dim, in_dim, dx != 0);
   const Fp8Plan g = plan(a.M, a.Nc, a.nk);
   const size_t need = lora_fp8_product_workspace_bytes(x, out_dim, in_dim, dx);
   if (need && (!ws || ws_bytes < need || !al16(ws))) return LORA_E_WORKSPACE;
-  a.Q = (const uint8_t*)x->data;
-  a.E = a.Q + off;
-  a.ldw = rup(in_dim, 128);
-  a.W = (const uint8_t*)W;
-  a.S = (const float*)(a.W + rup(out_dim, 128) * a.ldw);
-  a.lds_ = a.ldw / 128;
   a.C = out;
   a.part = (float*)ws;
-  a.ldq = (int64_t)a.nk * 128;
-  a.lde = rup(a.M, 128);
   a.per = g.per;
   a.nsplit = g.nsplit;
   const Fp8Cfg& c = kCfg[g.cfg];

@@ -32,6 +32,7 @@
 #include <utility>
 
 #include "common.hpp"
+#include "fp8_launch.hpp"
 
 namespace lora {
 
@@ -49,6 +50,8 @@ struct Fp8Args {
   int nk;                // contraction steps
   int per;               // steps of a split
   int nsplit;
+  Fp8Lora lora;          // OUT 3
+  float* C2;             // OUT 3: a second copy of the result, or NULL
 };
 
 // Place of token t's exponent within a contraction block's lde of them: of
@@ -109,7 +112,32 @@ LORA_DEV uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2_t));
 }
 
-// OUT: 0 float32, 1 bf16 (round to nearest even), 2 float32 partials.
+// Eight neighbours of a row of n float32 values (a multiple of 4 of them) from
+// index k, as bf16 (zero past the row).
+LORA_DEV u32x4 row_bf16(const float* row, int64_t k, int64_t n, float mul) {
+  f32x4 v[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const bool in = k + 4 * q < n;
+    v[q] = *reinterpret_cast<const f32x4*>(row + (in ? k + 4 * q : 0)) * (in ? mul : 0.0f);
+  }
+  return u32x4{pack2(v[0][0], v[0][1]), pack2(v[0][2], v[0][3]), pack2(v[1][0], v[1][1]),
+               pack2(v[1][2], v[1][3])};
+}
+// Eight values of a column, ld apart.
+LORA_DEV u32x4 col_bf16(const float* col, int64_t k, int64_t n, int64_t ld) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool in = k + e < n;
+    v[e] = in ? col[(k + e) * ld] : 0.0f;
+  }
+  return u32x4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
+}
+
+// OUT: 0 float32, 1 bf16 (round to nearest even), 2 float32 partials, 3
+// float32 with the LoRA term, whose factors are rounded to bf16 as in the
+// products over a bf16 W.
 template <int BM, int BN, int WM, int WN, int NS, bool DX, int OUT>
 __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)   // the host pass has no use for the body
@@ -258,6 +286,32 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
 
   // Tile (i, j) holds columns n0 + wn + 16 i + 4 h + v of token 16 j + c.
   const int64_t nb = n0 + wn;
+  if constexpr (OUT == 3) {
+    const Fp8Lora& l = p.lora;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int64_t t = min(m0 + wm + 16 * j + c, p.M - 1);
+      f32x4 d[TN];
+#pragma unroll
+      for (int i = 0; i < TN; ++i) d[i] = f32x4{0, 0, 0, 0};
+      for (int64_t k = 0; k < l.r; k += 32) {
+        const bf16x8 u = __builtin_bit_cast(bf16x8, row_bf16(l.lu + t * l.r, k + 8 * h, l.r, l.ls));
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          const int64_t n = min(nb + 16 * i + c, p.Nc - 1);
+          const u32x4 b = DX ? col_bf16(l.lb + n, k + 8 * h, l.r, p.Nc)
+                             : row_bf16(l.lb + n * l.r, k + 8 * h, l.r, 1.0f);
+          d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), u, d[i], 0, 0, 0);
+        }
+      }
+      const uint64_t row = DX && l.drop.on ? drop_row(l.drop, t) : 0;
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          acc[i][j][v] += DX && l.drop.on ? d[i][v] * drop_mul(l.drop, row, nb + 16 * i + 4 * h + v) : d[i][v];
+    }
+  }
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
     const int64_t t = m0 + wm + 16 * j + c;
@@ -292,11 +346,13 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
       }
     } else {
       float* row = (OUT == 2 ? p.part + (int64_t)split * p.M * p.Nc : (float*)p.C) + (in ? t : 0) * p.Nc;
+      float* row2 = OUT == 3 && p.C2 ? p.C2 + (in ? t : 0) * p.Nc : nullptr;
 #pragma unroll
       for (int i = 0; i < TN; ++i) {
         const int64_t n = nb + 16 * i + 4 * h;
         if (p.Nc % 4 == 0) {
           if (in && n < p.Nc) *reinterpret_cast<f32x4*>(row + n) = acc[i][j];
+          if (row2 && in && n < p.Nc) *reinterpret_cast<f32x4*>(row2 + n) = acc[i][j];
         } else {
 #pragma unroll
           for (int v = 0; v < 4; ++v)

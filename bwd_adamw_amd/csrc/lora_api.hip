@@ -14,6 +14,7 @@
 
 #include "../../include/lora.h"
 #include "common.hpp"
+#include "fp8_launch.hpp"
 #include "fused.hpp"
 #include "gemm_bf16.hpp"
 #include "gemm_f32.hpp"
@@ -35,7 +36,9 @@ inline int64_t clampi(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : 
 inline bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // bf16 or block-quantized W: the frozen products run on bf16 MFMA.
-inline bool bf16_ops(int32_t w_dtype) { return w_dtype != LORA_F32; }
+inline bool bf16_ops(int32_t w_dtype) { return w_dtype != LORA_F32 && w_dtype != LORA_FP8; }
+// 8-bit W: they run on 8-bit MFMA, over activations rounded to e4m3.
+inline bool fp8_ops(int32_t w_dtype) { return w_dtype == LORA_FP8; }
 
 // Planes of a block-quantized W [N, K] in one buffer: offset and size of
 // each (a missing plane sits at the end with size 0); returns the total, 0
@@ -325,6 +328,7 @@ struct Layout {
   bool vreduce;        // V partials summed by a separate launch
   size_t upart, xbf, gfpart;                          // forward
   size_t vpart, v, dbpart, dmpart, gbf, gdpart, dapart;   // backward
+  size_t x8, g8;       // 8-bit W: the rounded X (forward) and g (backward)
   size_t keep;         // the dropout mask's keep bits, ceil(K/32) x T words (k4 -> dX)
   size_t fwd_bytes, bwd_bytes;
 };
@@ -347,8 +351,14 @@ Layout make_layout(const lora_linear* L, int stack = 1) {
   y.strips = cdiv(N, SK_C);
   const int rpad = rank_pad(r);
   y.k4 = plan_rows(T, cdiv(K, SK_C), k4_slots(rpad));
-  y.gf = plan_gemm(stack * T, N, K, bf, false, tiled_ok(L, K));
-  y.gd = plan_gemm(stack * T, K, N, bf, true, tiled_ok(L, N));
+  const bool f8 = fp8_ops(L->w_dtype);
+  if (f8) {   // the 8-bit products plan themselves (fp8.hip), never split here
+    y.gf = {128, 128, {K, 1}, -1};
+    y.gd = {128, 128, {N, 1}, -1};
+  } else {
+    y.gf = plan_gemm(stack * T, N, K, bf, false, tiled_ok(L, K));
+    y.gd = plan_gemm(stack * T, K, N, bf, true, tiled_ok(L, N));
+  }
   // k3 beside the split dX GEMM keeps its own grid (one strip per block
   // there); the plain path groups strips.
   if (use_split_path(y.gd, r, bf)) {
@@ -386,11 +396,13 @@ Layout make_layout(const lora_linear* L, int stack = 1) {
     y.down = {len, (int)cdiv(K, len)};
   }
   const double vbytes = 4.0 * y.k3nvp * T * r;
-  y.vreduce = y.k3nvp > 1 && vbytes * (cdiv(K, y.gd.bn) + cdiv(K, SK_C)) > kPartialRereadBytes;
+  y.vreduce = y.k3nvp > 1 &&
+              (f8 || vbytes * (cdiv(K, y.gd.bn) + cdiv(K, SK_C)) > kPartialRereadBytes);
   size_t off = 0;
   y.upart = carve(off, y.down.n > 1 ? sizeof(float) * y.down.n * T * r : 0);
   y.xbf = carve(off, (bf && own) ? sizeof(uint16_t) * T * K : 0);
   y.gfpart = carve(off, (own && y.gf.k.n > 1) ? sizeof(float) * y.gf.k.n * T * N : 0);
+  y.x8 = carve(off, f8 ? fp8_operand_bytes(T, K) : 0);
   y.fwd_bytes = off;
   off = 0;
   y.vpart = carve(off, y.k3nvp > 1 ? sizeof(float) * y.k3nvp * T * r : 0);
@@ -402,6 +414,7 @@ Layout make_layout(const lora_linear* L, int stack = 1) {
   y.dapart = carve(off, y.k4.n > 1 ? sizeof(float) * y.k4.n * r * K : 0);
   // dX on the direct-operand loop takes the LoRA term's mask as bits that
   // k4 (which hashes every element of X anyway) leaves behind.
+  y.g8 = carve(off, f8 ? fp8_operand_bytes(T, N) : 0);
   y.keep = carve(off, (bf && plan_tiled(y.gd)) ? sizeof(uint32_t) * T * cdiv(K, 32) : 0);
   y.bwd_bytes = off;
   return y;
@@ -436,7 +449,14 @@ int check_linear(const lora_linear* L) {
   if (L->tokens <= 0 || L->in_dim <= 0 || L->out_dim <= 0 || L->rank <= 0) return LORA_E_SHAPE;
   if (L->rank > 128 || L->rank > L->in_dim || L->rank > L->out_dim) return LORA_E_SHAPE;
   const int32_t f = L->w_dtype;
-  if (f != LORA_F32 && f != LORA_BF16 && !wq_quantized(f)) return LORA_E_DTYPE;
+  if (f != LORA_F32 && f != LORA_BF16 && !wq_quantized(f) && !fp8_ops(f)) return LORA_E_DTYPE;
+  // 8-bit W: the layouts' own limits; DoRA's row norms do not read it.
+  if (fp8_ops(f)) {
+    if (!lora_fp8_weight_layout(L->out_dim, L->in_dim, nullptr) ||
+        !fp8_operand_bytes(L->tokens, L->in_dim) || !fp8_operand_bytes(L->tokens, L->out_dim))
+      return LORA_E_SHAPE;
+    if (L->dora_mag || L->dora_norm) return LORA_E_DTYPE;
+  }
   // bf16 operands and W's planes are read with 32-bit byte offsets (for
   // quantized W also from rows a tile past the end: in_dim <= 2^22).
   if (bf16_ops(f) &&
@@ -613,6 +633,8 @@ struct FwdJob {
   uint16_t* Xbf;
   const float* X;
   float *Y, *Z, *gfpart;
+  void* x8;         // 8-bit W: the rounded X ...
+  bool x8_ready;    // ... which another linear of the group has written
   RedJob ured;      // U's split partials summed once before the product, if has_ured
   bool has_ured;
 };
@@ -664,7 +686,10 @@ int prepare_fwd(const lora_linear* lin, const float* X, float* Y, float* U, floa
   // The direct-operand product stages U once per column of tiles: it reads
   // U summed by one reduction launch rather than summing the partials in
   // every tile.
-  j.has_ured = bf && !j.split && y.down.n > 1 && plan_tiled(y.gf);
+  const bool f8 = fp8_ops(lin->w_dtype);
+  j.x8 = f8 ? w + y.x8 : nullptr;
+  j.x8_ready = false;
+  j.has_ured = (f8 || (bf && !j.split && plan_tiled(y.gf))) && y.down.n > 1;
   if (j.has_ured) {
     j.ured = RedJob{Upart, U, nullptr, T * r, 1, (int)y.down.n, 0, 1.0f, 1};
     j.xa = LoraOperand{U, T * r, 1, nullptr};
@@ -762,6 +787,10 @@ void launch_fwd_plain(const FwdJob& j, hipStream_t st) {
     a.sl[0] = bf16_fwd_slot(j);
     a.ksplit = j.gf.k.len; a.nsplit = j.gf.k.n; a.part = j.gfpart;
     launch_gemm_bf16(j.gf, true, a, st);
+  } else if (fp8_ops(lin->w_dtype)) {
+    if (!j.x8_ready) fp8_launch_quantize(j.X, T, K, j.x8, st);
+    fp8_launch_lora_product(j.x8, T, lin->W, N, K, false, {j.xa.p, lin->B, r, lin->scale, {}}, j.Y,
+                            j.Z, st);
   } else {
     GemmF32Args a;
     memset(&a, 0, sizeof(a));
@@ -1082,6 +1111,10 @@ void launch_bwd_plain(const BwdJob& jb, hipStream_t st) {
       a.ksplit = y.gd.k.len; a.nsplit = y.gd.k.n;
       a.part = y.gd.k.n > 1 ? (float*)(jb.w + y.gdpart) : nullptr;
       launch_gemm_bf16(y.gd, false, a, st);
+    } else if (fp8_ops(lin->w_dtype)) {
+      fp8_launch_quantize(jb.dY, T, N, jb.w + y.g8, st);
+      fp8_launch_lora_product(jb.w + y.g8, T, lin->W, N, K, true,
+                              {jb.xv.p, lin->A, r, lin->scale, jb.d}, jb.dX, nullptr, st);
     } else {
       GemmF32Args a;
       memset(&a, 0, sizeof(a));
@@ -1247,6 +1280,12 @@ int lora_forward_group(int n, const lora_linear* lins, const float* X, float* co
     if (rc) return rc;
     off += wi;
   }
+  // The 8-bit linears of a group share one rounded X.
+  for (int i = 0, first = -1; i < n; ++i)
+    if (jobs[i].x8) {
+      if (first < 0) first = i;
+      else jobs[i].x8 = jobs[first].x8, jobs[i].x8_ready = true;
+    }
   hipStream_t st = (hipStream_t)stream;
   if (n == 2 && jobs[0].split && jobs[1].split) {
     launch_fwd_split<2>(jobs, st);

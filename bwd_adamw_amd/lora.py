@@ -37,7 +37,7 @@ __all__ = [
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblora.so")
 
-F32, BF16 = 0, 1
+F32, BF16, FP8 = 0, 1, 8
 # Block-quantized W formats (lora_dtype): code and plane names in layout order.
 Q_FORMATS = {"q8_0": (2, ("qs", "d")), "q4_0": (3, ("qs", "d")),
              "q4_k": (4, ("qs", "sm", "dm")), "q6_k": (5, ("ql", "qh", "sc", "d"))}
@@ -268,16 +268,16 @@ def qweight_pack(fmt: str, out_dim: int, in_dim: int, planes: dict, device="cuda
 
 def make_linear(W, A, B, scale, tokens, dora_mag=None, dora_norm=None,
                 dora_from_y=False) -> LoraLinear:
-    """Descriptor of one adapted linear: W [N,K] (float32 or bfloat16, or a
-    QWeight), A [r,K], B [N,r] float32, optional DoRA magnitude and norm [N].
+    """Descriptor of one adapted linear: W [N,K] (float32 or bfloat16, a
+    QWeight or an Fp8Weight), A [r,K], B [N,r] float32, optional DoRA magnitude and norm [N].
     dora_from_y (DoRA only): the backward takes the forward's Y where it
     would take Z, so the forward need not write Z."""
-    if isinstance(W, QWeight):
+    if isinstance(W, (QWeight, Fp8Weight)):
         wd = W.code
     elif W.dtype in (torch.float32, torch.bfloat16):
         wd = F32 if W.dtype == torch.float32 else BF16
     else:
-        raise TypeError(f"W must be float32, bfloat16 or a QWeight, got {W.dtype}")
+        raise TypeError(f"W must be float32, bfloat16, a QWeight or an Fp8Weight, got {W.dtype}")
     N, K = W.shape
     r = A.shape[0] if A is not None else 0
     if A is not None and tuple(A.shape) != (r, K):
@@ -287,7 +287,8 @@ def make_linear(W, A, B, scale, tokens, dora_mag=None, dora_norm=None,
     for t, nm in ((dora_mag, "dora_mag"), (dora_norm, "dora_norm")):
         if t is not None and t.numel() != N:
             raise ValueError(f"{nm} must hold {N} elements, got {t.numel()}")
-    wptr = _ptr(W.buf, "W", torch.uint8) if isinstance(W, QWeight) else _ptr(W, "W", None)
+    wptr = (_ptr(W.buf, "W", torch.uint8) if isinstance(W, (QWeight, Fp8Weight))
+            else _ptr(W, "W", None))
     return LoraLinear(int(tokens), int(K), int(N), int(r), wd, float(scale), wptr,
                       _ptr(A, "A"), _ptr(B, "B"), _ptr(dora_mag, "dora_mag"),
                       _ptr(dora_norm, "dora_norm"), 1 if dora_from_y else 0)
@@ -342,6 +343,7 @@ def lora_backward(lin, X, dY, U, Z, dX, dA, dB, dMag=None, accumulate=False, dro
 
 MAX_GROUP = 4
 MAX_SLOTS = 4
+MAX_RUNS = 32
 
 
 def _linears(lins):
@@ -647,6 +649,8 @@ class Fp8Weight:
     """An 8-bit W [out_dim, in_dim] in the library's layout (include/lora.h):
     one uint8 device buffer, e4m3 values in whole 128 x 128 blocks, then the
     blocks' float32 scales."""
+
+    code = FP8
 
     def __init__(self, out_dim: int, in_dim: int, buf: torch.Tensor):
         total, _ = lora_fp8_weight_layout(out_dim, in_dim)

@@ -8,7 +8,8 @@ accumulation"; "8. LoRA Fundamentals", "The training loop"):
       backward of every adapted linear, layers L-1..0 (gradients summed
       into the slot's arena; chunk 0 overwrites, later chunks add)
   prepare: global norm in double, non-finite veto, one combined scale
-  AdamW over the arena (A decayed, B at lr*ratio, DoRA magnitude)
+  AdamW over the arena (A decayed, B at lr*ratio, DoRA magnitude), or the
+  orthogonalised update of A and B (optimizer "muon")
   DoRA: refresh the detached row norms with the updated A, B
 
 Each slot ("Multi-LoRA Training Example (fully-async)", "Design") owns its
@@ -33,19 +34,23 @@ __all__ = ["FrozenModel", "Slot", "Trainer"]
 
 def _w_desc(W):
     """lora_dtype code and device address of a frozen weight (a float32 or
-    bfloat16 tensor, or a QWeight)."""
-    if isinstance(W, L.QWeight):
+    bfloat16 tensor, a QWeight or an Fp8Weight)."""
+    if isinstance(W, (L.QWeight, L.Fp8Weight)):
         return W.code, W.buf.data_ptr()
     return (L.BF16 if W.dtype == torch.bfloat16 else L.F32), W.data_ptr()
 
 
 class FrozenModel:
     """The frozen weights of every adapted linear, keyed (layer, proj ordinal):
-    float32 or bfloat16 tensors, or block-quantized QWeights."""
+    float32 or bfloat16 tensors, block-quantized QWeights or 8-bit Fp8Weights.
+    norms, keyed (layer, x_group), are the frozen norms whose outputs the
+    groups read: (kind, eps, gamma, beta or None) as make_norm takes them.
+    A group with a norm takes the norm's input as its X."""
 
-    def __init__(self, cfg: LoraConfig, weights: dict):
+    def __init__(self, cfg: LoraConfig, weights: dict, norms: dict | None = None):
         self.cfg = cfg
         self.W = weights
+        self.norms = norms or {}
         self.keys = sorted(weights)
         self.shape = {}
         for key in self.keys:
@@ -92,6 +97,20 @@ class Slot:
                 self.gmag[key] = self.grads[om:om + N]
                 om += N
         self.norm = {}
+        # The factors as runs of equal matrices (one projection's over the
+        # layers, where those are evenly spaced) for the orthogonalised update.
+        self.runs = []
+        for kind, mats in ((L.KIND_A, self.A), (L.KIND_B, self.B)):
+            for o in sorted({k[1] for k in self.keys}):
+                ms = [mats[k] for k in self.keys if k[1] == o]
+                at = [m.storage_offset() for m in ms]
+                step = at[1] - at[0] if len(at) > 1 else 0
+                same = all(m.shape == ms[0].shape for m in ms)
+                even = all(b - a == step for a, b in zip(at, at[1:]))
+                if same and even:
+                    self.runs.append(L.make_matrix_run(at[0], *ms[0].shape, len(at), step, kind))
+                else:
+                    self.runs += [L.make_matrix_run(a, *m.shape, kind=kind) for a, m in zip(at, ms)]
         self.t = 0   # applied updates
         self.k = 0   # 0-based index of the next update (schedule, dropout step)
 
@@ -126,7 +145,8 @@ class Trainer:
         # per product) when the library can: bf16 or quantized W and whole
         # 256-row tiles.
         self.nslots = int(slots)
-        self.stack_slots = (self.nslots > 1 and cfg.w_dtype != "f32" and self.T % 256 == 0)
+        self.stack_slots = (self.nslots > 1 and cfg.w_dtype not in ("f32", "fp8")
+                            and self.T % 256 == 0)
         self.scale = L.lora_scaling(cfg.alpha, cfg.rank, cfg.scaling == "rslora")
         self.device = device
         f32 = dict(device=device, dtype=torch.float32)
@@ -166,6 +186,23 @@ class Trainer:
                 a["dX"][key] = torch.empty(self.T, K, **f32)
             self.acts.append(a)
         self.U, self.Y, self.dX = (self.acts[0][n] for n in ("U", "Y", "dX"))
+        # Norms before the groups: their output, row statistics and the
+        # gradient of their input, by the group's index.
+        self.norms = {}
+        for gi, g in enumerate(self.groups):
+            nm = model.norms.get((g[0][0], xg[g[0][1]]))
+            if nm is None:
+                continue
+            if self.stack_slots:
+                raise ValueError("norms before the groups need unstacked slots")
+            kind, eps, gamma, beta = nm
+            K = model.shape[g[0]][0]
+            desc = L.make_norm(kind, self.T, K, torch.float32, eps, gamma, beta)
+            self.norms[gi] = (desc, torch.empty(self.T, K, **f32), torch.empty(self.T, 2, **f32),
+                              torch.empty(self.T, K, **f32), (gamma, beta))
+        # dH[(layer, x_group)]: gradient of a norm's input after forward_backward
+        self.dH = {(self.groups[gi][0][0], xg[self.groups[gi][0][1]]): n[3]
+                   for gi, n in self.norms.items()}
         self.ws = torch.empty(max(ws, 256), device=device, dtype=torch.uint8)
         # Streams beyond the current one (default priority), each with a
         # workspace; no more streams than units to spread (layer groups; layers
@@ -180,6 +217,9 @@ class Trainer:
         self.d_scale = torch.zeros(1, **f32)
         self.d_stats = torch.zeros(2, device=device, dtype=torch.float64)
         self.prep_ws = None
+        self.muon_ws = None
+        if cfg.optimizer not in ("adamw", "muon"):
+            raise ValueError(f"unknown optimizer {cfg.optimizer!r}")
 
     # ------------------------------------------------------------------
     def _linear(self, key, slot, dora=False, norms_only=False):
@@ -296,11 +336,21 @@ class Trainer:
                                           for k in keys])
                       for gi, keys in enumerate(self.groups)]
             for gi, keys in enumerate(self.groups):
-                calls[gi].forward(chunk[keys[0]][0], dr[gi])
+                X = chunk[keys[0]][0]
+                if gi in self.norms:
+                    desc, Xn, stats = self.norms[gi][:3]
+                    L.lora_norm_forward(desc, X, Xn, stats, stream=streams[gi % len(streams)])
+                    X = Xn
+                calls[gi].forward(X, dr[gi])
             for gi in reversed(range(ng)):
                 keys = self.groups[gi]
-                calls[gi].backward(chunk[keys[0]][0], [chunk[k][1] for k in keys],
+                X = self.norms[gi][1] if gi in self.norms else chunk[keys[0]][0]
+                calls[gi].backward(X, [chunk[k][1] for k in keys],
                                    accumulate=g > 0, drops=dr[gi])
+                if gi in self.norms:   # the group's gradients of X meet in the norm's backward
+                    desc, _, stats, dH = self.norms[gi][:4]
+                    L.lora_norm_backward(desc, chunk[keys[0]][0], [self.dX[k] for k in keys], stats,
+                                         dH, stream=streams[gi % len(streams)])
         self._join()
 
     def forward_backward_slots(self, slots: list, chunks_per_slot: list):
@@ -392,7 +442,19 @@ class Trainer:
             raise
         hp = L.LoraAdamwHparams(lr, cfg.beta1, cfg.beta2, cfg.eps, cfg.weight_decay,
                                 cfg.plus_ratio, slot.t + 1)
-        L.lora_adamw_step(slot.params, slot.grads, slot.m, slot.v, slot.segments, hp, self.d_scale)
+        segments = slot.segments
+        if cfg.optimizer == "muon":   # A and B; DoRA's magnitudes stay with AdamW
+            mu = L.make_muon(lr, cfg.momentum, cfg.weight_decay, cfg.plus_ratio, adjust="rms")
+            for i in range(0, len(slot.runs), L.MAX_RUNS):
+                runs = slot.runs[i:i + L.MAX_RUNS]
+                need = L.lora_muon_workspace_bytes(runs)
+                if self.muon_ws is None or self.muon_ws.numel() < need:
+                    self.muon_ws = torch.empty(need, device=self.device, dtype=torch.uint8)
+                L.lora_muon_step(slot.params, slot.grads, slot.m, runs, mu, self.d_scale,
+                                 self.muon_ws)
+            segments = [sg for sg in segments if sg[2] == L.KIND_MAG]
+        if segments:
+            L.lora_adamw_step(slot.params, slot.grads, slot.m, slot.v, segments, hp, self.d_scale)
         if cfg.dora and refresh:
             self.refresh_dora([slot])
         slot.t += 1

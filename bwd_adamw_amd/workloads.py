@@ -33,6 +33,7 @@ __all__ = [
     "draw",
     "linear_inputs",
     "qweight_planes",
+    "fp8_weight",
 ]
 
 
@@ -58,7 +59,7 @@ class LoraConfig:
     rank: int = 8
     alpha: float = 16.0
     scaling: str = "standard"   # or "rslora"
-    w_dtype: str = "f32"        # "bf16", or a block-quantized format (bench --w-format)
+    w_dtype: str = "f32"        # "bf16", "fp8", or a block-quantized format (bench --w-format)
     w_std: float = 0.02
     x_std: float = 1.0
     dy_std: float = 1.0
@@ -77,6 +78,8 @@ class LoraConfig:
     beta1: float = 0.9
     beta2: float = 0.999
     eps: float = 1e-8
+    optimizer: str = "adamw"    # or "muon" (lora_muon_step on A and B)
+    momentum: float = 0.95      # muon's
 
     @property
     def tokens_per_step(self) -> int:
@@ -194,6 +197,19 @@ def qweight_planes(fmt: str, N: int, K: int, key: tuple, device="cpu") -> dict:
                 "sc": _ints((N, K // 16), -32, 32, torch.int8, key, 2, device),
                 "d": _halves((N, K // 256), 2.0 ** -14, 2.0 ** -13, key, 3, device)}
     raise ValueError(f"unknown format {fmt!r}")
+
+
+def fp8_weight(W: torch.Tensor):
+    """(e4m3 values [N, K], scales [ceil(N/128), ceil(K/128)]) of a weight:
+    each 128 x 128 block divided by its largest value / 448."""
+    N, K = W.shape
+    nb, kb = -(-N // 128), -(-K // 128)
+    t = torch.zeros(nb * 128, kb * 128, device=W.device)
+    t[:N, :K] = W
+    t = t.view(nb, 128, kb, 128)
+    scale = t.abs().amax((1, 3)).clamp_min(1e-30) / 448
+    q = (t / scale[:, None, :, None]).view(nb * 128, kb * 128)[:N, :K]
+    return q.to(torch.float8_e4m3fn), scale
 
 
 def linear_inputs(cfg: LoraConfig, layer: int, proj: Projection, slot: int = 0,

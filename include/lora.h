@@ -79,7 +79,8 @@ typedef enum lora_dtype {
   LORA_Q8_0 = 2,
   LORA_Q4_0 = 3,
   LORA_Q4_K = 4,
-  LORA_Q6_K = 5
+  LORA_Q6_K = 5,
+  LORA_FP8 = 8              /* e4m3 with block scales: lora_fp8_weight_layout */
 } lora_dtype;
 
 /* Train-only inverted dropout on the LoRA-branch input ("4.3. Training
@@ -112,13 +113,18 @@ typedef struct lora_dropout {
  * 16-byte aligned (LORA_E_ALIGN otherwise).  bf16 and quantized W also need
  * in_dim*out_dim, tokens*in_dim and tokens*out_dim below 2^30 (their operands
  * are addressed with 32-bit byte offsets; LORA_E_SHAPE otherwise), and
- * quantized W an in_dim that is a whole number of its blocks (LORA_E_SHAPE). */
+ * quantized W an in_dim that is a whole number of its blocks (LORA_E_SHAPE).
+ * An 8-bit W (LORA_FP8, laid out by lora_fp8_weight_layout) runs its products
+ * as lora_fp8_quantize and lora_fp8_product do, on X and dY rounded to e4m3
+ * per block, with the LoRA factors rounded to bf16; it takes no DoRA
+ * (LORA_E_DTYPE), and neither the row norms nor the merge read it. */
 typedef struct lora_linear {
   int64_t tokens, in_dim, out_dim, rank;
   int32_t w_dtype;          /* lora_dtype                                  */
   float scale;              /* alpha/rank or alpha/sqrt(rank)              */
   const void* W;            /* [N,K] float32 or bf16, or the planes of a
-                               quantized W laid out by lora_qweight_layout */
+                               quantized W laid out by lora_qweight_layout
+                               (8-bit W: by lora_fp8_weight_layout)         */
   const float* A;           /* [r,K]                                       */
   const float* B;           /* [N,r]                                       */
   const float* dora_mag;    /* [N] or NULL                                 */
