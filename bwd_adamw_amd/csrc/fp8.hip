@@ -13,22 +13,27 @@ using namespace lora::host;
 
 namespace {
 
-// Tiles: tokens, columns, wave grid, stages in LDS (128, 128 and 60 KB of
+// Tiles: tokens, columns, wave grid, stages in LDS (130, 66 and 63 KB of
 // them), blocks a CU holds, and the time of one contraction step of a CU's
-// resident blocks and of a block's ends, in microseconds.
+// resident blocks and of a block's ends, in microseconds, fitted to all three
+// on the Qwen3-4B-shaped products at 128 to 4096 tokens.  4096 tokens of
+// [2560 -> 4096] forward: 43, 56 and 96 us; 512 of them 34, 25 and 15; 1000
+// of [2056 -> 1368] 28, 23 and 12.
 struct Fp8Cfg {
   int bm, bn, per_cu;
   double step, ends;
 };
 #define LORA_FP8_CFGS(X)                          \
-  X(0, 256, 256, 2, 4, 2, 1, 1.7, 6.0)            \
-  X(1, 128, 128, 2, 2, 2, 2, 1.1, 5.0)            \
-  X(2, 32, 128, 1, 4, 3, 2, 0.6, 4.0)
+  X(0, 256, 256, 2, 4, 2, 1, 1.5, 13.0)           \
+  X(1, 128, 128, 2, 2, 2, 2, 0.95, 7.0)           \
+  X(2, 32, 128, 1, 4, 3, 2, 0.42, 5.0)
 constexpr Fp8Cfg kCfg[] = {
 #define LORA_FP8_ROW(i, bm, bn, wm, wn, ns, pc, st, en) {bm, bn, pc, st, en},
     LORA_FP8_CFGS(LORA_FP8_ROW)
 #undef LORA_FP8_ROW
 };
+
+constexpr int kNCfg = sizeof(kCfg) / sizeof(kCfg[0]);
 
 struct Fp8Plan {
   int cfg, per, nsplit;
@@ -37,7 +42,7 @@ struct Fp8Plan {
 Fp8Plan plan(int64_t M, int64_t Nc, int nk, int most = 16) {
   Fp8Plan best = {0, nk, 1};
   double tb = 1e30;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < kNCfg; ++i) {
     const Fp8Cfg& c = kCfg[i];
     const int64_t tiles = cdiv(M, c.bm) * cdiv(Nc, c.bn);
     for (int want = 1; want <= std::min(nk, most); ++want) {
@@ -45,7 +50,8 @@ Fp8Plan plan(int64_t M, int64_t Nc, int nk, int most = 16) {
       if (n != want) continue;
       const double rounds = (double)cdiv(tiles * n, kCUs * c.per_cu);
       double t = rounds * (per * c.step + c.ends);
-      if (n > 1) t += 3.0 + 4.0 * M * Nc * (2.0 * n) / 4e6;
+      // Split partials: written, read, and summed by a launch of its own.
+      if (n > 1) t += 2.5 + 4.0 * M * Nc * (1.6 * n) / 5e6;
       if (t < tb) {
         tb = t;
         best = {i, per, n};
@@ -73,6 +79,11 @@ int check_fp8(const lora_fp8_operand* x, int64_t N, int64_t K, int dx) {
     return LORA_E_SHAPE;
   return LORA_OK;
 }
+
+// Few tokens, forward: up to 32 run without stages or splits (one launch; 64
+// ran no faster than the 32-token tiles).
+constexpr int64_t kFewTokens = 32;
+bool few(int64_t M, bool dx) { return !dx && M <= kFewTokens; }
 
 // Everything but the output and the split of a product.
 Fp8Args product_args(const void* x, int64_t rows, const void* W, int64_t N, int64_t K, bool dx) {
@@ -187,6 +198,7 @@ size_t lora_fp8_product_workspace_bytes(const lora_fp8_operand* x, int64_t out_d
                                         int dx) {
   if (check_fp8(x, out_dim, in_dim, dx) != LORA_OK) return 0;
   const int64_t Nc = dx ? in_dim : out_dim;
+  if (few(x->rows, dx)) return 0;
   const Fp8Plan g = plan(x->rows, Nc, (int)cdiv(x->cols, 128));
   return g.nsplit > 1 ? sizeof(float) * (size_t)(g.nsplit * x->rows * Nc) : 0;
 }
@@ -199,6 +211,22 @@ int lora_fp8_product(const lora_fp8_operand* x, const void* W, int64_t out_dim, 
   if (!x->data || !W || !out) return LORA_E_INVALID;
   if (!al16(x->data) || !al16(W) || !al16(out)) return LORA_E_ALIGN;
   Fp8Args a = product_args(x->data, x->rows, W, out_dim, in_dim, dx != 0);
+  if (few(a.M, dx)) {
+    a.C = out;
+    const bool bf = out_dtype == LORA_BF16;
+    prof::Scope ps("fp8_few_fwd", a.M, a.Nc, x->cols, 2.0 * a.M * a.Nc * x->cols,
+                   (double)a.M * a.ldq + (double)out_dim * in_dim + (bf ? 2.0 : 4.0) * a.M * a.Nc);
+    const dim3 grid((unsigned)cdiv(a.Nc, 16));
+    hipStream_t st = (hipStream_t)stream;
+    if (a.M <= 16) {
+      if (bf) launch_n(fp8_few_kernel<1, true>, grid, 512u, st, ps, a);
+      else launch_n(fp8_few_kernel<1, false>, grid, 512u, st, ps, a);
+    } else {
+      if (bf) launch_n(fp8_few_kernel<2, true>, grid, 512u, st, ps, a);
+      else launch_n(fp8_few_kernel<2, false>, grid, 512u, st, ps, a);
+    }
+    return hip_status();
+  }
   const Fp8Plan g = plan(a.M, a.Nc, a.nk);
   const size_t need = lora_fp8_product_workspace_bytes(x, out_dim, in_dim, dx);
   if (need && (!ws || ws_bytes < need || !al16(ws))) return LORA_E_WORKSPACE;

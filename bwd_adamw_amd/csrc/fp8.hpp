@@ -130,7 +130,8 @@ LORA_DEV u32x4 col_bf16(const float* col, int64_t k, int64_t n, int64_t ld) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const bool in = k + e < n;
-    v[e] = in ? col[(k + e) * ld] : 0.0f;
+    const float x = col[(in ? k + e : 0) * ld];   // unconditional: no wait in between
+    v[e] = in ? x : 0.0f;
   }
   return u32x4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
 }
@@ -143,6 +144,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)   // the host pass has no use for the body
   constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr int XB = BM * 128, WB = BN * 128, STAGE = XB + WB + 1024;   // X, W, exponents
+  constexpr bool MIX = TM == 4;
   constexpr int XL = XB / 1024 / NW, WL = WB / 1024 / NW;   // loads a wave and stage
   static_assert(XB % (1024 * NW) == 0 && WB % (1024 * NW) == 0, "whole loads per wave");
   static_assert(TM >= 1 && TN >= 1 && (BN / WN) <= 128 && 128 % (BN / WN) == 0, "one W scale a wave");
@@ -267,16 +269,47 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
         wf[i] = frag_rows(W + (wn + 16 * i) * 128, wo[0], wo[1]);
       }
     }
-    unrolled<TM>([&](auto J_) {
-      constexpr int J = decltype(J_)::value;
-      const i32x8 xf = frag_rows(X + 16 * J * 128, xo[0], xo[1]);
+    if constexpr (MIX) {
+      // Token tile J's MFMAs go out between the FMAs of tile J - 1, one with
+      // four FMAs each, and the reads of tile J + 1.  The 128-wide tile
+      // gains up to 9 % by it; the 256-wide one loses up to 10 % against the
+      // compiler's own order.
+      f32x4 d[2][TN];
+      i32x8 xf[2];
+      xf[0] = frag_rows(X, xo[0], xo[1]);
+      auto add = [&](auto J_) {
+        constexpr int J = decltype(J_)::value;
 #pragma unroll
-      for (int i = 0; i < TN; ++i) {
-        const f32x4 d = mfma_fp8_at<J>(wf[i], xf, ex);
+        for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][J][v] = fmaf(d[v], sw, acc[i][J][v]);
-      }
-    });
+          for (int v = 0; v < 4; ++v) acc[i][J][v] = fmaf(d[J & 1][i][v], sw, acc[i][J][v]);
+      };
+      unrolled<TM>([&](auto J_) {
+        constexpr int J = decltype(J_)::value;
+        if constexpr (J + 1 < TM) xf[(J + 1) & 1] = frag_rows(X + 16 * (J + 1) * 128, xo[0], xo[1]);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) d[J & 1][i] = mfma_fp8_at<J>(wf[i], xf[J & 1], ex);
+        if constexpr (J > 0) add(std::integral_constant<int, J - 1>{});
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if constexpr (J > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          if (i < 2 && J + 1 < TM) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+      });
+      add(std::integral_constant<int, TM - 1>{});
+    } else {
+      unrolled<TM>([&](auto J_) {
+        constexpr int J = decltype(J_)::value;
+        const i32x8 xf = frag_rows(X + 16 * J * 128, xo[0], xo[1]);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          const f32x4 d = mfma_fp8_at<J>(wf[i], xf, ex);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][J][v] = fmaf(d[v], sw, acc[i][J][v]);
+        }
+      });
+    }
     sw = wscale(k + 1);
     // Stage k + 1 is in once only the later stages' loads remain.
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * (XL + WL)) : "memory");
@@ -288,28 +321,46 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
   const int64_t nb = n0 + wn;
   if constexpr (OUT == 3) {
     const Fp8Lora& l = p.lora;
+    int64_t t[TM];
+    uint32_t keep[TM];   // dX: mask bits of the lane's 4 TN results a token
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int64_t t = min(m0 + wm + 16 * j + c, p.M - 1);
-      f32x4 d[TN];
+      t[j] = min(m0 + wm + 16 * j + c, p.M - 1);
+      keep[j] = 0xffffffffu;
+      if (DX && l.drop.on) {
+        const uint64_t row = drop_row(l.drop, t[j]);
+        keep[j] = 0;
 #pragma unroll
-      for (int i = 0; i < TN; ++i) d[i] = f32x4{0, 0, 0, 0};
-      for (int64_t k = 0; k < l.r; k += 32) {
-        const bf16x8 u = __builtin_bit_cast(bf16x8, row_bf16(l.lu + t * l.r, k + 8 * h, l.r, l.ls));
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            keep[j] |= (uint32_t)drop_keep(l.drop, row, nb + 16 * i + 4 * h + v) << (4 * i + v);
+      }
+    }
+    const float mul = DX && l.drop.on ? l.drop.keep : 1.0f;
+    for (int64_t k = 0; k < l.r; k += 32) {
+      bf16x8 b[TN], u[TM];
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        const int64_t n = min(nb + 16 * i + c, p.Nc - 1);
+        b[i] = __builtin_bit_cast(bf16x8, DX ? col_bf16(l.lb + n, k + 8 * h, l.r, p.Nc)
+                                             : row_bf16(l.lb + n * l.r, k + 8 * h, l.r, 1.0f));
+      }
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+        u[j] = __builtin_bit_cast(bf16x8, row_bf16(l.lu + t[j] * l.r, k + 8 * h, l.r, l.ls * mul));
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
 #pragma unroll
         for (int i = 0; i < TN; ++i) {
-          const int64_t n = min(nb + 16 * i + c, p.Nc - 1);
-          const u32x4 b = DX ? col_bf16(l.lb + n, k + 8 * h, l.r, p.Nc)
-                             : row_bf16(l.lb + n * l.r, k + 8 * h, l.r, 1.0f);
-          d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), u, d[i], 0, 0, 0);
+          if constexpr (DX) {
+            const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], u[j], f32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][j][v] += (keep[j] >> (4 * i + v)) & 1 ? d[v] : 0.0f;
+          } else {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], u[j], acc[i][j], 0, 0, 0);
+          }
         }
-      }
-      const uint64_t row = DX && l.drop.on ? drop_row(l.drop, t) : 0;
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          acc[i][j][v] += DX && l.drop.on ? d[i][v] * drop_mul(l.drop, row, nb + 16 * i + 4 * h + v) : d[i][v];
     }
   }
 #pragma unroll
@@ -361,6 +412,96 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
       }
     }
   }
+#endif
+}
+
+// Forward for few tokens (serving's single one, short chunks): bound by W's
+// bytes and by latency, so no LDS stages and no second launch.  A block takes
+// 16 columns; its eight waves take every eighth contraction step, with the
+// next two steps' fragments loading straight into registers, and their sums
+// meet in LDS in wave order.  W's rows are read in 64-byte pieces, two of a
+// step making whole lines.  TM: tiles of 16 tokens.
+template <int TM, bool BF16>
+__global__ __launch_bounds__(512) void fp8_few_kernel(Fp8Args p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NW = 8;
+  __shared__ f32x4 sum[NW][TM][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, h = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const uint8_t* wrow = p.W + (n0 + c) * p.ldw + 16 * h;   // W has whole 128-blocks
+  const uint8_t* xrow[TM];
+  const uint8_t* erow[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int64_t t = min((int64_t)(16 * j + c), p.M - 1);
+    xrow[j] = p.Q + t * p.ldq + 16 * h;
+    erow[j] = p.E + fp8_scale_at(t);
+  }
+  const float* sp = p.S + (n0 / 128) * p.lds_;
+  struct Step {
+    u32x4 w[2], x[TM][2];
+    int e[TM];
+    float s;
+  };
+  auto load = [&](Step& f, int k) {
+    const int kk = min(k, p.nk - 1);   // past the end: the last step again, not added
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f.w[q] = *reinterpret_cast<const u32x4*>(wrow + 128 * (int64_t)kk + 64 * q);
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+        f.x[j][q] = *reinterpret_cast<const u32x4*>(xrow[j] + 128 * (int64_t)kk + 64 * q);
+    }
+#pragma unroll
+    for (int j = 0; j < TM; ++j) f.e[j] = erow[j][(int64_t)kk * p.lde];
+    f.s = sp[kk];
+  };
+  f32x4 acc[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) acc[j] = f32x4{0, 0, 0, 0};
+  auto add = [&](const Step& f) {
+    const i32x8 w = {(int)f.w[0][0], (int)f.w[0][1], (int)f.w[0][2], (int)f.w[0][3],
+                     (int)f.w[1][0], (int)f.w[1][1], (int)f.w[1][2], (int)f.w[1][3]};
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const i32x8 x = {(int)f.x[j][0][0], (int)f.x[j][0][1], (int)f.x[j][0][2], (int)f.x[j][0][3],
+                       (int)f.x[j][1][0], (int)f.x[j][1][1], (int)f.x[j][1][2], (int)f.x[j][1][3]};
+      const f32x4 d = mfma_fp8<0>(w, x, f.e[j]);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[j][v] = fmaf(d[v], f.s, acc[j][v]);
+    }
+  };
+  Step a, b, d;
+  int k = wave;
+  load(a, k);
+  load(b, k + NW);
+  while (k < p.nk) {   // three steps take turns
+    load(d, k + 2 * NW);
+    add(a);
+    if ((k += NW) >= p.nk) break;
+    load(a, k + 2 * NW);
+    add(b);
+    if ((k += NW) >= p.nk) break;
+    load(b, k + 2 * NW);
+    add(d);
+    k += NW;
+  }
+#pragma unroll
+  for (int j = 0; j < TM; ++j) sum[wave][j][lane] = acc[j];
+  __syncthreads();
+  if (wave >= TM) return;
+  f32x4 r = sum[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) r += sum[w][wave][lane];
+  const int64_t t = 16 * wave + c, n = n0 + 4 * h;
+  if (t >= p.M) return;
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (n + v < p.Nc) {
+      if constexpr (BF16) ((uint16_t*)p.C)[t * p.Nc + n + v] = (uint16_t)f32_to_bf16_bits(r[v]);
+      else ((float*)p.C)[t * p.Nc + n + v] = r[v];
+    }
 #endif
 }
 

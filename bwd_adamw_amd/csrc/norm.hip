@@ -193,7 +193,7 @@ int lora_norm_backward(const lora_norm* norm, const void* X, int n_dy, const voi
   }
   if (sums && g.blocks > 1) {
     prof::Scope ps("norm_finish", g.blocks, norm->dim, 1, 0.0, 8.0 * g.blocks * norm->dim);
-    launch_n(norm_finish_kernel, dim3((unsigned)cdiv(norm->dim, 32), 2u), 256u, st, ps,
+    launch_n(norm_finish_kernel, dim3((unsigned)cdiv(norm->dim, 32), dbeta ? 2u : 1u), 1024u, st, ps,
              (const float*)ws, (int)g.blocks, (int)norm->dim, dgamma, dbeta, a.accumulate);
   }
   return hip_status();

@@ -21,6 +21,8 @@
 // Float32 rows of 2560, 4096 of them (4.9 to 5.2 TB/s is what a plain copy
 // reaches): see the figures at the launches in norm.hip.
 #pragma once
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace lora {
@@ -197,7 +199,57 @@ __global__ __launch_bounds__(norm_threads(TPR)) void norm_fwd_kernel(NormArgs p)
   }
 }
 
-// NDY gradients of y (0: p.ndy of them, read one after another).
+// A row's operands as loaded: x and NDY gradients of y (0: the sum of p.ndy of
+// them, read element by element one after another).
+template <typename T, int TPR, int V, bool VEC, int NDY>
+struct NormRow {
+  typedef std::conditional_t<sizeof(T) == 4, f32x4, u32x2> Raw;
+  static constexpr int N = NDY ? NDY : 1;
+  static constexpr bool AHEAD = VEC && (1 + N) * V * (int)sizeof(T) <= 24;
+  std::conditional_t<VEC, Raw, f32x4> x[V], d[N][V];
+  f32x2 stats;
+
+  // Unconditional loads (columns past dim repeat the first ones; their dy is
+  // masked in dy()): a guarded load is waited for at the end of its branch.
+  LORA_DEV void load(const NormArgs& p, int64_t row, int t) {
+    const T* xr = (const T*)p.X + row * p.ldx;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        int c = norm_col<TPR, true>(i, 0, t);
+        c = c < p.dim ? c : 0;
+        x[i] = *reinterpret_cast<const Raw*>(xr + c);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          d[n][i] = *reinterpret_cast<const Raw*>((const T*)p.dY[n] + row * p.ldy + c);
+      }
+    } else {
+      norm_load<T, TPR, V, false>(x, xr, p.dim, t);
+      norm_load<T, TPR, V, false>(d[0], (const T*)p.dY[0] + row * p.ldy, p.dim, t);
+      for (int n = 1; n < p.ndy; ++n) {
+        const void* q = n == 1 ? p.dY[1] : n == 2 ? p.dY[2] : p.dY[3];
+        f32x4 e[V];
+        norm_load<T, TPR, V, false>(e, (const T*)q + row * p.ldy, p.dim, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[0][i] += e[i];
+      }
+    }
+    stats = *reinterpret_cast<const f32x2*>(p.stats + 2 * row);
+  }
+  template <typename R>
+  LORA_DEV static f32x4 value(R r) {
+    if constexpr (sizeof(R) == 16) return r;
+    else return f32x4{__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u),
+                      __uint_as_float(r[1] << 16), __uint_as_float(r[1] & 0xffff0000u)};
+  }
+  LORA_DEV f32x4 dy(int i, bool in) const {
+    f32x4 s = value(d[0][i]);
+#pragma unroll
+    for (int n = 1; n < N; ++n) s += value(d[n][i]);
+    return in ? s : f32x4{0, 0, 0, 0};
+  }
+};
+
 template <typename T, int TPR, int V, bool VEC, int NDY>
 __global__ __launch_bounds__(norm_threads(TPR)) void norm_bwd_kernel(NormArgs p) {
   constexpr int NT = norm_threads(TPR), R = NT / TPR, COLS = TPR * V * 4;
@@ -210,56 +262,64 @@ __global__ __launch_bounds__(norm_threads(TPR)) void norm_bwd_kernel(NormArgs p)
 #pragma unroll
   for (int i = 0; i < V; ++i) dg[i] = db[i] = f32x4{0, 0, 0, 0};
   int buf = 0;
-  for (int64_t base = r0; base < r1; base += R) {
-    const int64_t row = min(base + g, r1 - 1);
+  typedef NormRow<T, TPR, V, VEC, NDY> Row;
+  auto use = [&](const Row& q, int64_t base) {
     const bool mine = base + g < r1;
-    f32x4 x[V], dy[V];
-    norm_load<T, TPR, V, VEC>(x, (const T*)p.X + row * p.ldx, p.dim, t);
-    norm_load<T, TPR, V, VEC>(dy, (const T*)p.dY[0] + row * p.ldy, p.dim, t);
-    if constexpr (NDY > 1) {
-      f32x4 e[NDY - 1][V];
-#pragma unroll
-      for (int n = 1; n < NDY; ++n)
-        norm_load<T, TPR, V, VEC>(e[n - 1], (const T*)p.dY[n] + row * p.ldy, p.dim, t);
-#pragma unroll
-      for (int n = 1; n < NDY; ++n)
-#pragma unroll
-        for (int i = 0; i < V; ++i) dy[i] += e[n - 1][i];
-    } else if constexpr (NDY == 0) {
-      for (int n = 1; n < p.ndy; ++n) {
-        const void* q = n == 1 ? p.dY[1] : n == 2 ? p.dY[2] : p.dY[3];
-        f32x4 e[V];
-        norm_load<T, TPR, V, VEC>(e, (const T*)q + row * p.ldy, p.dim, t);
-#pragma unroll
-        for (int i = 0; i < V; ++i) dy[i] += e[i];
-      }
-    }
-    const f32x2 st = *reinterpret_cast<const f32x2*>(p.stats + 2 * row);
-    const float mean = st[0], rstd = st[1];
+    const float mean = q.stats[0], rstd = q.stats[1];
     // Columns past dim hold dy = 0 and drop out of every sum.
+    f32x4 x[V], dy[V];
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+      x[i] = Row::value(q.x[i]);
+      dy[i] = q.dy(i, mine && (!VEC || norm_col<TPR, true>(i, 0, t) < p.dim));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float xh = (x[i][e] - mean) * rstd, d = mine ? dy[i][e] : 0.0f;
+        const float xh = (x[i][e] - mean) * rstd, d = dy[i][e];
         x[i][e] = xh;
         dg[i][e] += d * xh;
         db[i][e] += d;
-        dy[i][e] *= ga[i][e];
+        dy[i][e] = d * ga[i][e];
         s1 += dy[i][e];
         s2 += dy[i][e] * xh;
       }
-    if (!p.out) continue;   // the same for every lane
+    }
+    if (!p.out) return;   // the same for every lane
     row_sum<TPR>(s1, s2, red, buf);
     s1 = p.layer ? s1 / p.fdim : 0.0f;
     s2 /= p.fdim;
-    if (!mine) continue;
+    if (!mine) return;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[i][e] = rstd * (dy[i][e] - s1 - x[i][e] * s2);
-    norm_store<T, TPR, V, VEC>((T*)p.out + row * p.ldx, x, p.dim, t);
+    norm_store<T, TPR, V, VEC>((T*)p.out + (base + g) * p.ldx, x, p.dim, t);
+  };
+  // Lanes past the last row repeat it.  Where a row is a few registers the
+  // next one loads while one is used (1537 x 4100 bf16, one gradient: 27 -> 19
+  // us); with more, the waves that fit fewer registers hide as much (4096 x
+  // 2560 float32, three gradients: 44 us against 40).
+  auto at = [&](int64_t base) { return min(base + g, r1 - 1); };
+  int64_t base = r0;
+  if constexpr (Row::AHEAD) {
+    Row a, b;
+    a.load(p, at(base), t);
+    for (;;) {
+      if (base + R < r1) b.load(p, at(base + R), t);
+      __builtin_amdgcn_sched_barrier(0);
+      use(a, base);
+      if ((base += R) >= r1) break;
+      if (base + R < r1) a.load(p, at(base + R), t);
+      __builtin_amdgcn_sched_barrier(0);
+      use(b, base);
+      if ((base += R) >= r1) break;
+    }
+  } else {
+    for (; base < r1; base += R) {
+      Row a;
+      a.load(p, at(base), t);
+      use(a, base);
+    }
   }
   if (!p.dgamma && !p.dbeta) return;
   // Sum the block's R row groups in group order, gamma then beta.
@@ -299,12 +359,12 @@ __global__ __launch_bounds__(norm_threads(TPR)) void norm_bwd_kernel(NormArgs p)
 }
 
 // dgamma / dbeta from the blocks' partials: a block takes 32 columns of one
-// of the two, eight threads a column (each every eighth partial, in order),
-// in double.
-__global__ __launch_bounds__(256) void norm_finish_kernel(const float* __restrict__ part, int parts,
-                                                          int dim, float* dgamma, float* dbeta,
-                                                          int accumulate) {
-  __shared__ double red[8][33];
+// of the two, 32 threads a column (each every 32nd partial, in order), in
+// double.
+__global__ __launch_bounds__(1024) void norm_finish_kernel(const float* __restrict__ part, int parts,
+                                                           int dim, float* dgamma, float* dbeta,
+                                                           int accumulate) {
+  __shared__ double red[32][33];
   const int cx = threadIdx.x & 31, py = threadIdx.x >> 5;
   float* out = blockIdx.y == 0 ? dgamma : dbeta;
   if (!out) return;
@@ -313,13 +373,13 @@ __global__ __launch_bounds__(256) void norm_finish_kernel(const float* __restric
   if (c < dim) {
     const float* q = part + (int64_t)blockIdx.y * dim + c;
 #pragma unroll 8
-    for (int i = py; i < parts; i += 8) s += (double)q[(int64_t)i * 2 * dim];
+    for (int i = py; i < parts; i += 32) s += (double)q[(int64_t)i * 2 * dim];
   }
   red[py][cx] = s;
   __syncthreads();
   if (py == 0 && c < dim) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][cx];
+    for (int i = 1; i < 32; ++i) s += red[i][cx];
     out[c] = (float)(accumulate ? (double)out[c] + s : s);
   }
 }

@@ -121,7 +121,7 @@ def weight(N, K, seed, whole):
 
 # Tokens, inputs, outputs: every tile size, splits of the contraction, ragged
 # in each direction.
-SHAPES = [(1, 1, 1), (1, 128, 128), (1, 2560, 4096), (7, 300, 40), (33, 640, 264), (40, 4096, 130),
+SHAPES = [(1, 1, 1), (1, 128, 128), (1, 2560, 4096), (7, 300, 40), (17, 9728, 260), (32, 260, 520), (33, 640, 264), (40, 4096, 130),
           (128, 1024, 1024), (129, 1000, 257), (200, 136, 2000), (1000, 2056, 1368), (255, 384, 512),
           (600, 256, 1100), (2048, 640, 2560), (2100, 200, 2600), (4096, 128, 4200)]
 
@@ -257,7 +257,7 @@ def test_invalid_arguments_are_refused():
     assert prod(op(cols=1 << 20), n=1 << 20, k=1 << 20) == -2
     assert prod(op(), dt=3) == -3
     assert prod(op(), W=264) == -4 and prod(op(), out=8) == -4 and prod(op(data=8)) == -4
-    big = lambda: op(rows=1, cols=9728)
+    big = lambda: op(rows=64, cols=9728)
     need = lib.lora_fp8_product_workspace_bytes(big(), 256, 9728, 0)
     assert need > 0
     assert prod(big(), n=256, k=9728, size=need - 1) == -5
