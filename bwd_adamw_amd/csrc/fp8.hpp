@@ -46,6 +46,7 @@ struct Fp8Args {
   void* C;               // [M, Nc] float32 or bf16
   float* part;           // [nsplit][M][Nc] when nsplit > 1
   int64_t M, Nc;
+  int64_t ldc;           // elements between rows of C
   int64_t ldq, lde, ldw, lds_;   // bytes a row of Q, W and a block of E; floats a row of S
   int nk;                // contraction steps
   int per;               // steps of a split
@@ -185,8 +186,8 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
     if constexpr (DX) {
       constexpr int CPR = BN / 16;
       const int slot = 64 * (wave * WL + q) + lane, row = slot / CPR, ch = (slot % CPR) ^ (row & 7);
-      // Columns past W's padded row: the tile's first ones instead.
-      vw[q] = (uint32_t)(row * p.ldw) + (n0 + 16 * ch < p.ldw ? 16 * ch : 0);
+      // Columns past the last 128-block: the tile's first ones instead.
+      vw[q] = (uint32_t)(row * p.ldw) + (n0 + 16 * ch < (p.Nc + 127) / 128 * 128 ? 16 * ch : 0);
     } else {
       const int row = 8 * (wave * WL + q) + (lane >> 3);
       vw[q] = (uint32_t)(min((int64_t)row, wrows - 1) * p.ldw) + 16 * ((lane & 7) ^ (row & 7));
@@ -216,7 +217,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
           rE, (__attribute__((address_space(3))) void*)(b + XB + WB), 4, ve, (int)(kk * p.lde), 0, 0);
   };
   const int64_t sblk = (n0 + wn) / 128;
-  const float* sp = DX ? p.S + min(sblk, p.lds_ - 1) : p.S + min(sblk, (p.Nc - 1) / 128) * p.lds_;
+  const float* sp = p.S + min(sblk, (p.Nc - 1) / 128) * (DX ? 1 : p.lds_);
   // (constant address space: a scalar load, off the vector memory counter)
   typedef const __attribute__((address_space(4))) float* const_f32;
   auto wscale = [&](int k) {
@@ -368,8 +369,8 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
     const int64_t t = m0 + wm + 16 * j + c;
     const bool in = t < p.M;
     if constexpr (OUT == 1) {
-      uint16_t* row = (uint16_t*)p.C + (in ? t : 0) * p.Nc;
-      if (TN % 2 == 0 && p.Nc % 8 == 0) {
+      uint16_t* row = (uint16_t*)p.C + (in ? t : 0) * p.ldc;
+      if (TN % 2 == 0 && p.ldc % 8 == 0) {
         // Tiles i and i + 1 swap between neighbouring lane groups, so that a
         // lane stores eight columns of one of them.
 #pragma unroll
@@ -396,12 +397,13 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
           }
       }
     } else {
-      float* row = (OUT == 2 ? p.part + (int64_t)split * p.M * p.Nc : (float*)p.C) + (in ? t : 0) * p.Nc;
+      float* row = OUT == 2 ? p.part + ((int64_t)split * p.M + (in ? t : 0)) * p.Nc
+                            : (float*)p.C + (in ? t : 0) * p.ldc;
       float* row2 = OUT == 3 && p.C2 ? p.C2 + (in ? t : 0) * p.Nc : nullptr;
 #pragma unroll
       for (int i = 0; i < TN; ++i) {
         const int64_t n = nb + 16 * i + 4 * h;
-        if (p.Nc % 4 == 0) {
+        if ((OUT == 2 ? p.Nc : p.ldc) % 4 == 0) {
           if (in && n < p.Nc) *reinterpret_cast<f32x4*>(row + n) = acc[i][j];
           if (row2 && in && n < p.Nc) *reinterpret_cast<f32x4*>(row2 + n) = acc[i][j];
         } else {

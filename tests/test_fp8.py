@@ -123,7 +123,9 @@ def weight(N, K, seed, whole):
 # in each direction.
 SHAPES = [(1, 1, 1), (1, 128, 128), (1, 2560, 4096), (7, 300, 40), (17, 9728, 260), (32, 260, 520), (33, 640, 264), (40, 4096, 130),
           (128, 1024, 1024), (129, 1000, 257), (200, 136, 2000), (1000, 2056, 1368), (255, 384, 512),
-          (600, 256, 1100), (2048, 640, 2560), (2100, 200, 2600), (4096, 128, 4200)]
+          (600, 256, 1100), (2048, 640, 2560), (2100, 200, 2600), (4096, 128, 4200),
+          # whole rounds of the largest tile, then the other columns
+          (4096, 2560, 4360), (3000, 2056, 6000)]
 
 
 @gpu
