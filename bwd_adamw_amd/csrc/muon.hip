@@ -27,7 +27,7 @@ struct Class {          // the runs of one padded short side
   int64_t blocks, mats;
   double elems, flops;
   bool vec;
-  size_t part, poly, bytes;
+  size_t part, poly, mem, bytes;
   bool small;
 };
 
@@ -111,12 +111,14 @@ bool plan_class(const lora_matrix_run* runs, int n, int rp, const lora_muon_hpar
   off += (size_t)rup(blk * tiles(rp) * 64 * 32, 256);
   c.poly = off;
   off += (size_t)rup(mat * rp * rp * 8, 256);
+  c.mem = off;
+  if (rp == 128) off += (size_t)(mat * PolyMem<128>::BYTES);
   c.bytes = off;
   return true;
 }
 
 template <int RP, bool VEC, bool MUON>
-void launch_class(const Class& c, hipStream_t st) {
+void launch_class(const Class& c, char* ws, hipStream_t st) {
   const double e = 4.0 * c.elems, part = 32.0 * 64 * tiles(RP) * c.blocks;
   if constexpr (RP == 16) {
     if (c.small) {
@@ -133,7 +135,22 @@ void launch_class(const Class& c, hipStream_t st) {
     prof::Scope ps("muon_gram", c.mats, RP, c.blocks, c.flops, (MUON ? 3 : 1) * e + part);
     launch(muon_gram_kernel<RP, VEC, MUON>, dim3((unsigned)c.blocks), st, ps, c.a);
   }
-  {
+  if constexpr (RP == 128) {
+    char* mem = ws + c.mem;
+    {
+      prof::Scope ps("muon_assemble", c.mats, RP, c.blocks, 0.0, part);
+      launch(muon_assemble_kernel<RP>, dim3((unsigned)(c.mats * tiles(RP) / 4)), st, ps, c.a, mem);
+    }
+    for (int k = 0; k < c.a.steps; ++k) {
+      const bool last = k + 1 == c.a.steps;
+      for (int phase = 0; phase < 3; ++phase) {
+        if (last && (phase == 2 || (phase == 1 && k == 0))) continue;
+        const int64_t n = c.mats * tiles(RP) * (phase == 1 && k > 0 && !last ? 2 : 1);
+        prof::Scope ps("muon_product", c.mats, RP, phase, 2.0 * 256 * RP * n, 24.0 * 256 * n);
+        launch(muon_product_kernel<RP>, dim3((unsigned)(n / 4)), st, ps, c.a, mem, phase, k);
+      }
+    }
+  } else {
     prof::Scope ps("muon_poly", c.mats, RP, c.a.steps, 8.0 * c.a.steps * c.mats * RP * RP * RP,
                    part + 8.0 * c.mats * RP * RP);
     launch_n(muon_poly_kernel<RP>, dim3((unsigned)c.mats), 64u * poly_nw<RP>(), st, ps, c.a);
@@ -143,11 +160,11 @@ void launch_class(const Class& c, hipStream_t st) {
   launch(muon_apply_kernel<RP, VEC, MUON>, dim3((unsigned)c.blocks), st, ps, c.a);
 }
 template <bool MUON>
-void launch_rp(int rp, const Class& c, hipStream_t st) {
+void launch_rp(int rp, const Class& c, char* ws, hipStream_t st) {
 #define LORA_MUON_RP(RP_)                                       \
   if (rp == RP_) {                                              \
-    if (c.vec) launch_class<RP_, true, MUON>(c, st);            \
-    else launch_class<RP_, false, MUON>(c, st);                 \
+    if (c.vec) launch_class<RP_, true, MUON>(c, ws, st);        \
+    else launch_class<RP_, false, MUON>(c, ws, st);             \
   }
   LORA_MUON_RP(16) LORA_MUON_RP(32) LORA_MUON_RP(64) LORA_MUON_RP(128)
 #undef LORA_MUON_RP
@@ -174,8 +191,8 @@ int run_all(const lora_matrix_run* runs, int n, const lora_muon_hparams* h, cons
     c.a.a = h->a;
     c.a.b = h->b;
     c.a.c = h->c;
-    if (M) launch_rp<true>(rp, c, (hipStream_t)stream);
-    else launch_rp<false>(rp, c, (hipStream_t)stream);
+    if (M) launch_rp<true>(rp, c, (char*)ws, (hipStream_t)stream);
+    else launch_rp<false>(rp, c, (char*)ws, (hipStream_t)stream);
   }
   return hip_status();
 }

@@ -9,8 +9,9 @@
 // tall matrix is the transpose: G_0 = X^T X, X_n = X P.)  Three launches:
 //   gram   u from the gradient and the momentum (which it updates), and the
 //          upper half of u u^T by blocks of columns; reads g, m, writes m
-//   poly   one block a matrix: sums the blocks' partials in order, takes the
-//          norm from the trace, iterates Q and G in LDS, leaves P
+//   poly   one block a matrix (at R > 64 a launch a product): sums the blocks'
+//          partials in order, takes the norm from the trace, iterates Q and G,
+//          leaves P
 //   apply  P u and the parameter update; reads g, m, p, writes p
 // against the 2 n passes over X of the iteration as written.
 //
@@ -343,27 +344,26 @@ __global__ __launch_bounds__(256, muon_per_cu<RP>()) void muon_gram_kernel(MuonA
 // of two such matrices needs no rearrangement, only 16-byte LDS reads.
 //
 // The iteration takes 4 products a step (G^2, Q P, Q G, Q (Q G); the first
-// and last step fewer), 17 in all for five steps, on one CU, and is bound by
-// its float64 MFMA (32 to 35 ns an instruction and SIMD, measured).  Up to
-// RP 64 all matrices are in LDS (128 KB at 64) and only the upper tiles are
-// computed, 5/8 of them at 64; stores mirror them.  RP 128 has room for the
-// upper tiles of two matrices (144 KB): Q and the factor at hand, the others
-// in registers; reads of lower tiles transpose.
+// and last step fewer), 17 in all for five steps, and is bound by float64 MFMA
+// (32 to 35 ns an instruction and SIMD, measured).  Up to RP 64 one CU runs it
+// whole, all matrices in LDS (128 KB at 64), with only the upper tiles
+// computed, 5/8 of them at 64; stores mirror them.  At RP 128 that would be
+// 160 us of one CU's MFMA (275 us measured): there each product is a launch
+// with a wave for every upper tile (muon_product_kernel), 15 for five steps.
 template <int RP>
 struct PolyLds {
-  static constexpr int F = RP / 16, NM = F == 1 ? 1 : F == 8 ? 2 : 4;
-  // Tile (w, t) at (w F + t) 64; at F 8 the upper ones, one after another.
-  f64x4 a[NM][(F == 8 ? muon_tiles<RP>() : F * F) * 64];
+  static constexpr int F = RP / 16, NM = F == 1 ? 1 : 4;
+  f64x4 a[NM][F * F * 64];   // tile (w, t) at (w F + t) 64
   double diag[RP];
 };
 // Waves of poly_waves, and the barriers that they meet at.
 template <int RP>
 constexpr int poly_nw() {
-  return RP == 16 ? 1 : RP == 32 ? 4 : 8;
+  return RP == 16 ? 1 : RP == 32 ? 4 : 8;   // RP up to 64
 }
 template <int RP>
 LORA_DEV int poly_syncs(int steps) {
-  return RP == 16 ? 2 : 1 + 3 * steps;   // not used at 128
+  return RP == 16 ? 2 : 1 + 3 * steps;
 }
 
 // Tile (t, u) of A B.
@@ -398,9 +398,7 @@ LORA_DEV void poly_waves(const MuonArgs& p, bool wide, const f64x4* in, int spli
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, h = lane >> 4;
   double* const flat = reinterpret_cast<double*>(m.a[0]);
   auto at = [&](int i, int j) -> double& {
-    const int t = i >> 4, w = j >> 4;
-    const int tile = F == 8 ? t * F - t * (t - 1) / 2 + w - t : t * F + w;
-    return flat[(tile * 64 + (i & 3) * 16 + (j & 15)) * 4 + ((i >> 2) & 3)];
+    return flat[(((i >> 4) * F + (j >> 4)) * 64 + (i & 3) * 16 + (j & 15)) * 4 + ((i >> 2) & 3)];
   };
   // A tall matrix's fragment f holds columns F c + f.
   for (int i = wave; i < NT; i += NW) {
@@ -413,8 +411,8 @@ LORA_DEV void poly_waves(const MuonArgs& p, bool wide, const f64x4* in, int spli
     for (int v = 0; v < 4; ++v) {
       const int rc = 4 * v + h;
       const int row = wide ? 16 * t + rc : F * rc + t, col = wide ? 16 * w + c : F * c + w;
-      if (F < 8 || (row >> 4) <= (col >> 4)) at(row, col) = s[v];
-      if (F < 8 || (col >> 4) <= (row >> 4)) at(col, row) = s[v];
+      at(row, col) = s[v];
+      at(col, row) = s[v];
     }
   }
   sync();
@@ -495,7 +493,7 @@ LORA_DEV void poly_waves(const MuonArgs& p, bool wide, const f64x4* in, int spli
       }
       sync();
     }
-  } else if constexpr (F == 1) {
+  } else {
     f64x4 G = m.a[0][lane] * inv2, P = G;
     auto mul = [](f64x4 A, f64x4 B) {
       f64x4 d = {0, 0, 0, 0};
@@ -510,72 +508,6 @@ LORA_DEV void poly_waves(const MuonArgs& p, bool wide, const f64x4* in, int spli
     }
 #pragma unroll
     for (int v = 0; v < 4; ++v) out[(4 * v + h) * ldp + c] = P[v] * inv;
-  } else {
-    // Q and one other matrix in LDS, by their upper tiles; a wave keeps its
-    // own tiles of the others.
-    f64x4 *A = m.a[0], *Q = m.a[1];
-    constexpr int PER = (NT + NW - 1) / NW;
-    auto tile = [&](const f64x4* M, int t, int u) {
-      if (t <= u) return M[(t * F - t * (t - 1) / 2 + u - t) * 64 + lane];
-      const double* q = reinterpret_cast<const double*>(
-                            M + (u * F - u * (u - 1) / 2 + t - u) * 64 + (c & 3) * 16 + h) + (c >> 2);
-      return f64x4{q[0], q[16], q[32], q[48]};
-    };
-    auto mul = [&](const f64x4* L, const f64x4* R, int t, int u) {
-      f64x4 d = {0, 0, 0, 0};
-#pragma unroll 2
-      for (int w = 0; w < F; ++w) {
-        const f64x4 x = tile(L, w, t), y = tile(R, w, u);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) d = mfma16x16x4_f64(x[s], y[s], d);
-      }
-      return d;
-    };
-    auto mine = [&](auto fn) {   // this wave's tiles
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        const int i = wave + NW * q;
-        if (i < NT) {
-          int t, u;
-          muon_tile<RP>(i, t, u);
-          fn(q, i, t, u);
-        }
-      }
-    };
-    f64x4 P[PER], T[PER];
-    for (int k = 0; k < p.steps; ++k) {
-      const bool last = k + 1 == p.steps;
-      const double g1 = k == 0 ? inv2 : 1.0, g2 = g1 * g1;
-      mine([&](int q, int i, int t, int u) {
-        const f64x4 d = poly(mul(A, A, t, u) * g2, A[i * 64 + lane] * g1, t == u);
-        Q[i * 64 + lane] = d;
-        if (k == 0) P[q] = d;
-      });
-      sync();
-      if (!last) mine([&](int q, int, int t, int u) { T[q] = mul(Q, A, t, u) * g1; });
-      if (k > 0) {
-        sync();
-        mine([&](int q, int i, int, int) { A[i * 64 + lane] = P[q]; });
-        sync();
-        mine([&](int q, int, int t, int u) { P[q] = mul(Q, A, t, u); });
-      }
-      if (last) break;
-      sync();
-      mine([&](int q, int i, int, int) { A[i * 64 + lane] = T[q]; });
-      sync();
-      mine([&](int q, int, int t, int u) { T[q] = mul(Q, A, t, u); });
-      sync();
-      mine([&](int q, int i, int, int) { A[i * 64 + lane] = T[q]; });
-      sync();
-    }
-    mine([&](int q, int, int t, int u) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int row = 16 * t + 4 * v + h, col = 16 * u + c;
-        out[row * ldp + col] = P[q][v] * inv;
-        out[col * ldp + row] = P[q][v] * inv;
-      }
-    });
   }
 }
 
@@ -589,6 +521,107 @@ __global__ __launch_bounds__(64 * poly_nw<RP>()) void muon_poly_kernel(MuonArgs 
                     ((int64_t)r.blk0 + (int64_t)mat * r.splits) * muon_tiles<RP>() * 64;
   poly_waves<RP>(p, r.rows <= r.cols, in, r.splits, m, p.poly + (int64_t)blockIdx.x * RP * RP, RP,
                  [] { __syncthreads(); });
+}
+
+// RP 128: five matrices a mat in device memory, in the tiles of PolyLds.
+template <int RP>
+struct PolyMem {
+  static constexpr int F = RP / 16, SZ = F * F * 64;   // f64x4 a matrix
+  static constexpr int64_t BYTES = 5ll * SZ * 32 + 256;
+  f64x4* p;
+  LORA_DEV PolyMem(char* base, int mat) : p(reinterpret_cast<f64x4*>(base + mat * BYTES)) {}
+  LORA_DEV f64x4* G() const { return p; }
+  LORA_DEV f64x4* Q() const { return p + SZ; }
+  LORA_DEV f64x4* T() const { return p + 2 * SZ; }
+  LORA_DEV f64x4* P(int k) const { return p + (3 + (k & 1)) * SZ; }   // after step k
+  LORA_DEV double& inv() const { return *reinterpret_cast<double*>(p + 5 * SZ); }
+};
+
+// G from the blocks' partials, a wave an upper tile.
+template <int RP>
+__global__ __launch_bounds__(256) void muon_assemble_kernel(MuonArgs p, char* mem) {
+  constexpr int F = RP / 16, NT = muon_tiles<RP>();
+  static_assert(NT % 4 == 0, "whole blocks a matrix");
+  if (muon_vetoed(p)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int mi = wave / NT, i = wave % NT, lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
+  const MuonRun& r = p.run[muon_find(p, mi, true)];
+  const bool wide = r.rows <= r.cols;
+  const f64x4* in = reinterpret_cast<const f64x4*>(p.part) +
+                    ((int64_t)r.blk0 + (int64_t)(mi - r.mat0) * r.splits) * NT * 64 + i * 64 + lane;
+  f64x4 s = in[0];
+#pragma unroll 8
+  for (int q = 1; q < r.splits; ++q) s += in[(int64_t)q * NT * 64];
+  double* flat = reinterpret_cast<double*>(PolyMem<RP>(mem, mi).G());
+  auto at = [&](int i, int j) -> double& {
+    return flat[(((i >> 4) * F + (j >> 4)) * 64 + (i & 3) * 16 + (j & 15)) * 4 + ((i >> 2) & 3)];
+  };
+  int t, w;
+  muon_tile<RP>(i, t, w);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int rc = 4 * v + h;
+    const int row = wide ? 16 * t + rc : F * rc + t, col = wide ? 16 * w + c : F * c + w;
+    at(row, col) = s[v];
+    at(col, row) = s[v];
+  }
+}
+
+// One product of step k, a wave an upper tile.  phase 0: Q = a I + b G + c G^2
+// (and P at k 0); 1: T = Q G, and after them P <- Q P for k > 0 (the last step:
+// P alone); 2: G = Q T.  The last P goes to p.poly, divided by the norm.
+template <int RP>
+__global__ __launch_bounds__(256) void muon_product_kernel(MuonArgs p, char* mem, int phase, int k) {
+  constexpr int F = RP / 16, NT = muon_tiles<RP>();
+  static_assert(NT % 4 == 0, "whole blocks a matrix");
+  if (muon_vetoed(p)) return;
+  const bool last = k + 1 == p.steps, both = phase == 1 && k > 0 && !last;
+  const int jobs = both ? 2 * NT : NT;
+  const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int mat = wave / jobs, job = wave % jobs, lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
+  int t, u;
+  muon_tile<RP>(job % NT, t, u);
+  const PolyMem<RP> m(mem, mat);
+  double inv;
+  if (phase == 0 && k == 0) {   // the norm, from G's trace
+    double tr = 0.0;
+#pragma unroll
+    for (int i = lane; i < RP; i += 64)
+      tr += reinterpret_cast<const double*>(
+          m.G() + (i >> 4) * (F + 1) * 64 + (i & 3) * 16 + (i & 15))[(i >> 2) & 3];
+    const double norm = sqrt(wave_sum(tr)) + p.eps;
+    inv = norm > 0.0 || norm != norm ? 1.0 / norm : 0.0;   // a NaN stays one
+    if (job == 0 && lane == 0) m.inv() = inv;
+  } else {
+    inv = m.inv();
+  }
+  const double g1 = k == 0 ? inv * inv : 1.0;
+  const bool is_p = phase == 1 && (last || job >= NT);
+  f64x4* out;
+  f64x4 d;
+  if (phase == 0) {
+    d = sym_tile<F>(m.G(), m.G(), t, u, lane);
+    const f64x4 g = m.G()[(t * F + u) * 64 + lane];
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      d[v] = p.c * (g1 * g1) * d[v] + p.b * g1 * g[v] + (t == u && 4 * v + h == c ? p.a : 0.0);
+    out = m.Q();
+  } else {
+    d = sym_tile<F>(m.Q(), phase == 2 ? m.T() : is_p ? m.P(k - 1) : m.G(), t, u, lane);
+    if (phase == 1 && !is_p) d *= g1;
+    out = phase == 2 ? m.G() : is_p ? m.P(k) : m.T();
+  }
+  sym_store<F>(out, t, u, d, lane);
+  if (phase == 0 && k == 0) sym_store<F>(m.P(0), t, u, d, lane);
+  if (last && (is_p || (phase == 0 && k == 0))) {
+    double* poly = p.poly + (int64_t)mat * RP * RP;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int row = 16 * t + 4 * v + h, col = 16 * u + c;
+      poly[row * RP + col] = d[v] * inv;
+      poly[col * RP + row] = d[v] * inv;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ apply
