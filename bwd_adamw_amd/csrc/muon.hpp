@@ -366,6 +366,20 @@ LORA_DEV int poly_syncs(int steps) {
   return RP == 16 ? 2 : 1 + 3 * steps;
 }
 
+// s = the n values at `in`, stride apart, in order; eight loads at a time, all
+// of them unconditional (past the last one it is read again, and not added).
+LORA_DEV void sum_tiles(f64x4& s, const f64x4* in, int stride, int n) {
+  s = f64x4{0, 0, 0, 0};
+  for (int q = 0; q < n; q += 8) {
+    f64x4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = in[(int64_t)min(q + u, n - 1) * stride];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (q + u < n) s += v[u];
+  }
+}
+
 // Tile (t, u) of A B.
 template <int F>
 LORA_DEV f64x4 sym_tile(const f64x4* A, const f64x4* B, int t, int u, int lane) {
@@ -402,9 +416,8 @@ LORA_DEV void poly_waves(const MuonArgs& p, bool wide, const f64x4* in, int spli
   };
   // A tall matrix's fragment f holds columns F c + f.
   for (int i = wave; i < NT; i += NW) {
-    f64x4 s = in[i * 64 + lane];
-#pragma unroll 4
-    for (int q = 1; q < splits; ++q) s += in[((int64_t)q * NT + i) * 64 + lane];
+    f64x4 s;
+    sum_tiles(s, in + i * 64 + lane, NT * 64, splits);
     int t, w;
     muon_tile<RP>(i, t, w);
 #pragma unroll
@@ -549,9 +562,8 @@ __global__ __launch_bounds__(256) void muon_assemble_kernel(MuonArgs p, char* me
   const bool wide = r.rows <= r.cols;
   const f64x4* in = reinterpret_cast<const f64x4*>(p.part) +
                     ((int64_t)r.blk0 + (int64_t)(mi - r.mat0) * r.splits) * NT * 64 + i * 64 + lane;
-  f64x4 s = in[0];
-#pragma unroll 8
-  for (int q = 1; q < r.splits; ++q) s += in[(int64_t)q * NT * 64];
+  f64x4 s;
+  sum_tiles(s, in, NT * 64, r.splits);
   double* flat = reinterpret_cast<double*>(PolyMem<RP>(mem, mi).G());
   auto at = [&](int i, int j) -> double& {
     return flat[(((i >> 4) * F + (j >> 4)) * 64 + (i & 3) * 16 + (j & 15)) * 4 + ((i >> 2) & 3)];
