@@ -90,9 +90,11 @@ int check_fp8(const lora_fp8_operand* x, int64_t N, int64_t K, int dx) {
   return LORA_OK;
 }
 
-// Few tokens, forward: up to 32 run without stages or splits (one launch; 64
-// ran no faster than the 32-token tiles).
-constexpr int64_t kFewTokens = 32;
+// Few tokens, forward: up to one tile of 16 run without stages or splits, in
+// one launch.  One token of [2560 -> 4096]: 4.5 us against 7.6 of the 32-token
+// tiles and their sum; 16 tokens of [2560 -> 9728] 9.9 against 11.0; two such
+// tiles (32 tokens of [9728 -> 2560]) took 16.0 against 12.2.
+constexpr int64_t kFewTokens = 16;
 bool few(int64_t M, bool dx) { return !dx && M <= kFewTokens; }
 
 // Everything but the output and the split of a product.
@@ -228,13 +230,8 @@ int lora_fp8_product(const lora_fp8_operand* x, const void* W, int64_t out_dim, 
                    (double)a.M * a.ldq + (double)out_dim * in_dim + (bf ? 2.0 : 4.0) * a.M * a.Nc);
     const dim3 grid((unsigned)cdiv(a.Nc, 16));
     hipStream_t st = (hipStream_t)stream;
-    if (a.M <= 16) {
-      if (bf) launch_n(fp8_few_kernel<1, true>, grid, 512u, st, ps, a);
-      else launch_n(fp8_few_kernel<1, false>, grid, 512u, st, ps, a);
-    } else {
-      if (bf) launch_n(fp8_few_kernel<2, true>, grid, 512u, st, ps, a);
-      else launch_n(fp8_few_kernel<2, false>, grid, 512u, st, ps, a);
-    }
+    if (bf) launch_n(fp8_few_kernel<true>, grid, 512u, st, ps, a);
+    else launch_n(fp8_few_kernel<false>, grid, 512u, st, ps, a);
     return hip_status();
   }
   const Fp8Plan g = plan(a.M, a.Nc, a.nk);

@@ -28,6 +28,13 @@
 // ds_read_b64_tr_b8: even lanes of a group address the first eight columns of
 // a 16-wide tile in eight rows, odd lanes the other eight, which gives lane c
 // column c in those rows.
+//
+// Rate: the 256 x 256 tile runs 4096 tokens of [2560 -> 4096], one full round,
+// at 2.0 PFLOP/s (43 us); a step takes 1.5 us against the 1.0 that its MFMAs
+// need at the 4.2 PFLOP/s they reach alone.  The rest is the FMAs (four
+// for each MFMA, half its time, on the vector unit beside it) and the barrier
+// of each step.  Rounding moves 4 + 1 bytes a value at 5 TB/s (4096 x 2560:
+// 10.5 us).
 #pragma once
 #include <utility>
 
@@ -417,62 +424,50 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
 #endif
 }
 
-// Forward for few tokens (serving's single one, short chunks): bound by W's
-// bytes and by latency, so no LDS stages and no second launch.  A block takes
-// 16 columns; its eight waves take every eighth contraction step, with the
-// next two steps' fragments loading straight into registers, and their sums
-// meet in LDS in wave order.  W's rows are read in 64-byte pieces, two of a
-// step making whole lines.  TM: tiles of 16 tokens.
-template <int TM, bool BF16>
+// Forward for up to 16 tokens (serving's single one, the shortest chunks):
+// bound by W's bytes and by latency, so no LDS stages and no second launch.  A
+// block takes 16 columns; its eight waves take every eighth contraction step,
+// with the next two steps' fragments loading straight into registers, and
+// their sums meet in LDS in wave order.  W's rows are read in 64-byte pieces,
+// two of a step making whole lines.  One token of [2560 -> 4096]: 4.5 us for
+// 10.5 MB (2.3 TB/s, with the launch).
+template <bool BF16>
 __global__ __launch_bounds__(512) void fp8_few_kernel(Fp8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = 8;
-  __shared__ f32x4 sum[NW][TM][64];
+  __shared__ f32x4 sum[NW][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, h = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const uint8_t* wrow = p.W + (n0 + c) * p.ldw + 16 * h;   // W has whole 128-blocks
-  const uint8_t* xrow[TM];
-  const uint8_t* erow[TM];
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int64_t t = min((int64_t)(16 * j + c), p.M - 1);
-    xrow[j] = p.Q + t * p.ldq + 16 * h;
-    erow[j] = p.E + fp8_scale_at(t);
-  }
+  const int64_t tc = min((int64_t)c, p.M - 1);
+  const uint8_t* xrow = p.Q + tc * p.ldq + 16 * h;
+  const uint8_t* erow = p.E + fp8_scale_at(tc);
   const float* sp = p.S + (n0 / 128) * p.lds_;
   struct Step {
-    u32x4 w[2], x[TM][2];
-    int e[TM];
+    u32x4 w[2], x[2];
+    int e;
     float s;
   };
   auto load = [&](Step& f, int k) {
-    const int kk = min(k, p.nk - 1);   // past the end: the last step again, not added
+    const int64_t kk = min(k, p.nk - 1);   // past the end: the last step again, not added
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      f.w[q] = *reinterpret_cast<const u32x4*>(wrow + 128 * (int64_t)kk + 64 * q);
-#pragma unroll
-      for (int j = 0; j < TM; ++j)
-        f.x[j][q] = *reinterpret_cast<const u32x4*>(xrow[j] + 128 * (int64_t)kk + 64 * q);
+      f.w[q] = *reinterpret_cast<const u32x4*>(wrow + 128 * kk + 64 * q);
+      f.x[q] = *reinterpret_cast<const u32x4*>(xrow + 128 * kk + 64 * q);
     }
-#pragma unroll
-    for (int j = 0; j < TM; ++j) f.e[j] = erow[j][(int64_t)kk * p.lde];
+    f.e = erow[kk * p.lde];
     f.s = sp[kk];
   };
-  f32x4 acc[TM];
-#pragma unroll
-  for (int j = 0; j < TM; ++j) acc[j] = f32x4{0, 0, 0, 0};
+  f32x4 acc = {0, 0, 0, 0};
+  auto frag = [](const u32x4(&v)[2]) {
+    return i32x8{(int)v[0][0], (int)v[0][1], (int)v[0][2], (int)v[0][3],
+                 (int)v[1][0], (int)v[1][1], (int)v[1][2], (int)v[1][3]};
+  };
   auto add = [&](const Step& f) {
-    const i32x8 w = {(int)f.w[0][0], (int)f.w[0][1], (int)f.w[0][2], (int)f.w[0][3],
-                     (int)f.w[1][0], (int)f.w[1][1], (int)f.w[1][2], (int)f.w[1][3]};
+    const f32x4 d = mfma_fp8<0>(frag(f.w), frag(f.x), f.e);
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const i32x8 x = {(int)f.x[j][0][0], (int)f.x[j][0][1], (int)f.x[j][0][2], (int)f.x[j][0][3],
-                       (int)f.x[j][1][0], (int)f.x[j][1][1], (int)f.x[j][1][2], (int)f.x[j][1][3]};
-      const f32x4 d = mfma_fp8<0>(w, x, f.e[j]);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[j][v] = fmaf(d[v], f.s, acc[j][v]);
-    }
+    for (int v = 0; v < 4; ++v) acc[v] = fmaf(d[v], f.s, acc[v]);
   };
   Step a, b, d;
   int k = wave;
@@ -489,20 +484,19 @@ __global__ __launch_bounds__(512) void fp8_few_kernel(Fp8Args p) {
     add(d);
     k += NW;
   }
-#pragma unroll
-  for (int j = 0; j < TM; ++j) sum[wave][j][lane] = acc[j];
+  sum[wave][lane] = acc;
   __syncthreads();
-  if (wave >= TM) return;
-  f32x4 r = sum[0][wave][lane];
+  if (wave > 0) return;
+  f32x4 r = sum[0][lane];
 #pragma unroll
-  for (int w = 1; w < NW; ++w) r += sum[w][wave][lane];
-  const int64_t t = 16 * wave + c, n = n0 + 4 * h;
-  if (t >= p.M) return;
+  for (int w = 1; w < NW; ++w) r += sum[w][lane];
+  const int64_t n = n0 + 4 * h;
+  if (c >= p.M) return;
 #pragma unroll
   for (int v = 0; v < 4; ++v)
     if (n + v < p.Nc) {
-      if constexpr (BF16) ((uint16_t*)p.C)[t * p.Nc + n + v] = (uint16_t)f32_to_bf16_bits(r[v]);
-      else ((float*)p.C)[t * p.Nc + n + v] = r[v];
+      if constexpr (BF16) ((uint16_t*)p.C)[c * p.Nc + n + v] = (uint16_t)f32_to_bf16_bits(r[v]);
+      else ((float*)p.C)[c * p.Nc + n + v] = r[v];
     }
 #endif
 }

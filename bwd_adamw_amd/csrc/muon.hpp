@@ -21,7 +21,9 @@
 // would lose all but three digits.  In float64 the results are as accurate as
 // the float32 data, and the two passes still cost less MFMA time than memory
 // time up to R = 128 (2 R flops an element each, the first half of that by
-// symmetry, at 64 flops a byte and more).
+// symmetry, at 64 flops a byte and more).  Measured for 72 x [9728, 64]: gram
+// 110 us (543 MB, 4.9 TB/s), poly 38, apply 155 (724 MB, 4.7 TB/s); wide
+// matrices, whose rows are read in 64-byte pieces, 20 % slower.
 //
 // Fragments: a 16x16x4 operand is row l % 16 and contraction index l / 16 of
 // lane l, the same for both sides of a symmetric product, so one load serves
@@ -699,18 +701,21 @@ LORA_DEV void apply_range(const MuonArgs& p, const MuonRun& r, const double* P, 
          in ? min(N, (WIDE ? k1 : r.cols) - col) : 0);
     }
   };
-  int k = k0 + (wave / NP) * 16 * E;
+  // From the range's end to its start: what the gram pass read last is still
+  // in the last-level cache (256 MB).
+  const int kw = k0 + (wave / NP) * 16 * E;
+  int k = kw + (k1 - 1 - kw + STEP) / STEP * STEP - STEP;   // below kw: no chunk
   Chunk q;
-  if (k < k1) q.load(p, r, base, k, k1, lane);
+  if (k >= kw) q.load(p, r, base, k, k1, lane);
   __builtin_amdgcn_sched_barrier(0);
   ready();
-  for (; k < k1; k += STEP) {
+  for (; k >= kw; k -= STEP) {
     float x[Chunk::NS][N], w[MUON ? NO : 1][MUON ? N : 1];
     q.to_u(p, r, k, k1, lane, sc, x);
     // This chunk's parameters and the next chunk arrive during the products.
     if constexpr (MUON)
       results(k, [&](int i, uint32_t at, int n) { ldn<VEC, N>(w[i], p.P + base, at, n); });
-    if (k + STEP < k1) q.load(p, r, base, k + STEP, k1, lane);
+    if (k - STEP >= kw) q.load(p, r, base, k - STEP, k1, lane);
     __builtin_amdgcn_sched_barrier(0);
     f64x4 acc[FP][E];
 #pragma unroll

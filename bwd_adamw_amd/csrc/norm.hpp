@@ -18,8 +18,11 @@
 // block); they leave as one partial per block, which norm_finish_kernel adds
 // in block order in double.  One block writes the result itself.
 //
-// Float32 rows of 2560, 4096 of them (4.9 to 5.2 TB/s is what a plain copy
-// reaches): see the figures at the launches in norm.hip.
+// Measured (a plain copy moves 5.1 TB/s from HBM): 4096 rows of 2560 float32,
+// forward 13.5 us (84 MB, part of it from the last-level cache); backward of
+// three gradients 39.8 us (210 MB, 5.3 TB/s) and 4.7 for the sums of the
+// partials; 1537 x 4100 bf16, one gradient, 18.7 and 5.4 us (38 MB and 25 MB
+// of partials: few rows for the width).
 #pragma once
 #include <type_traits>
 
