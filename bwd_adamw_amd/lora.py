@@ -217,6 +217,20 @@ def _stream(stream):
     return int(stream)
 
 
+def _own_ws(need, device, stream):
+    """A workspace from torch's allocator for a call on `stream` (None: the
+    current one).  The memory is this binding's to give back, when the call
+    returns: on another stream than the current one the allocator has to be
+    told that it is still in use there."""
+    ws = torch.empty(need, device=device, dtype=torch.uint8)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                      else torch.cuda.default_stream(device))
+        ws.record_stream(stream)
+    return ws
+
+
 def _check(fn, rc):
     if rc != 0:
         raise LoraError(fn, rc)
@@ -718,7 +732,7 @@ def lora_fp8_product(x: Fp8Rows, W: Fp8Weight, out, dx=False, ws=None, stream=No
     if ws is None:
         need = lora_fp8_product_workspace_bytes(x, W, dx)
         if need:
-            ws = torch.empty(need, device=out.device, dtype=torch.uint8)
+            ws = _own_ws(need, out.device, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     rc = lib().lora_fp8_product(C.byref(x.desc), W.buf.data_ptr(), W.out_dim, W.in_dim,
                                 1 if dx else 0,
@@ -761,10 +775,9 @@ def lora_muon_workspace_bytes(runs) -> int:
     return int(lib().lora_muon_workspace_bytes(_runs(runs)[0], len(runs)))
 
 
-def _muon_ws(arr, n, ws, device):
+def _muon_ws(arr, n, ws, device, stream):
     if ws is None:
-        ws = torch.empty(max(16, int(lib().lora_muon_workspace_bytes(arr, n))), device=device,
-                         dtype=torch.uint8)
+        ws = _own_ws(max(16, int(lib().lora_muon_workspace_bytes(arr, n))), device, stream)
     return ws
 
 
@@ -773,7 +786,7 @@ def lora_orthogonalize(G, O, runs, hp: LoraMuonHparams, ws=None, stream=None):
     taken from torch's allocator when None."""
     arr, end = _runs(runs)
     g, o = _sized(G, "G", end), _sized(O, "O", end)
-    ws = _muon_ws(arr, len(runs), ws, G.device)
+    ws = _muon_ws(arr, len(runs), ws, G.device, stream)
     rc = lib().lora_orthogonalize(g, o, arr, len(runs), C.byref(hp), _ptr(ws, "ws", None),
                                   ws.numel() * ws.element_size(), _stream(stream))
     _check("lora_orthogonalize", rc)
@@ -784,7 +797,7 @@ def lora_muon_step(params, grads, m, runs, hp: LoraMuonHparams, d_scale, ws=None
     `ws` is taken from torch's allocator when None."""
     arr, end = _runs(runs)
     p, g, mo = _sized(params, "params", end), _sized(grads, "grads", end), _sized(m, "m", end)
-    ws = _muon_ws(arr, len(runs), ws, params.device)
+    ws = _muon_ws(arr, len(runs), ws, params.device, stream)
     rc = lib().lora_muon_step(p, g, mo, arr, len(runs), C.byref(hp), _sized(d_scale, "d_scale", 1),
                               _ptr(ws, "ws", None), ws.numel() * ws.element_size(),
                               _stream(stream))
@@ -858,7 +871,7 @@ def lora_norm_backward(norm: LoraNorm, X, dY, stats, dX=None, dgamma=None, dbeta
     if ws is None and (dgamma is not None or dbeta is not None):
         need = lora_norm_workspace_bytes(norm)
         if need:
-            ws = torch.empty(need, device=X.device, dtype=torch.uint8)
+            ws = _own_ws(need, X.device, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     rc = lib().lora_norm_backward(C.byref(norm), _rows_ptr(X, "X", r, d, norm.ldx, dt), len(dY),
                                   dys, _sized(stats, "stats", 2 * r),
