@@ -150,7 +150,7 @@ void launch_class(const Class& c, char* ws, hipStream_t st) {
         launch(muon_product_kernel<RP>, dim3((unsigned)(n / 4)), st, ps, c.a, mem, phase, k);
       }
     }
-  } else {
+  } else if constexpr (RP > 16) {   // at 16 the apply pass iterates it
     prof::Scope ps("muon_poly", c.mats, RP, c.a.steps, 8.0 * c.a.steps * c.mats * RP * RP * RP,
                    part + 8.0 * c.mats * RP * RP);
     launch_n(muon_poly_kernel<RP>, dim3((unsigned)c.mats), 64u * poly_nw<RP>(), st, ps, c.a);

@@ -11,7 +11,7 @@
 //          upper half of u u^T by blocks of columns; reads g, m, writes m
 //   poly   one block a matrix (at R > 64 a launch a product): sums the blocks'
 //          partials in order, takes the norm from the trace, iterates Q and G,
-//          leaves P
+//          leaves P; up to R 16 the apply blocks do it themselves
 //   apply  P u and the parameter update; reads g, m, p, writes p
 // against the 2 n passes over X of the iteration as written.
 //
@@ -759,17 +759,33 @@ __global__ __launch_bounds__(256, muon_per_cu<RP>()) void muon_apply_kernel(Muon
   const float sc = p.d_scale ? *p.d_scale : 1.0f;
   const MuonRun& r = p.run[muon_find(p, blockIdx.x, false)];
   const int rel = blockIdx.x - r.blk0, mat = rel / r.splits, sp = rel % r.splits;
-  typedef double f64x2 __attribute__((ext_vector_type(2)));
+  const bool wide = r.rows <= r.cols;
   auto ready = [&] {
-    const f64x2* src = reinterpret_cast<const f64x2*>(p.poly + (int64_t)(r.mat0 + mat) * RP * RP);
+    if constexpr (RP == 16) {
+      // The polynomial of a 16 x 16 matrix is 2 us of one wave: every block
+      // iterates its own, under its first chunk's loads, which saves a launch
+      // (22 x [8, 2048]: 16.8 -> 13.2 us).
+      __shared__ PolyLds<RP> m;
+      const f64x4* in = reinterpret_cast<const f64x4*>(p.part) +
+                        ((int64_t)r.blk0 + (int64_t)mat * r.splits) * muon_tiles<RP>() * 64;
+      auto sync = [] { __syncthreads(); };
+      if (threadIdx.x < 64) {
+        poly_waves<RP>(p, wide, in, r.splits, m, P, LDP, sync);
+      } else {
+        for (int i = 0; i < poly_syncs<RP>(p.steps); ++i) sync();
+      }
+    } else {
+      typedef double f64x2 __attribute__((ext_vector_type(2)));
+      const f64x2* src = reinterpret_cast<const f64x2*>(p.poly + (int64_t)(r.mat0 + mat) * RP * RP);
 #pragma unroll
-    for (int i = 2 * threadIdx.x; i < RP * RP; i += 512)
-      *reinterpret_cast<f64x2*>(P + (i / RP) * LDP + i % RP) = src[i / 2];
+      for (int i = 2 * threadIdx.x; i < RP * RP; i += 512)
+        *reinterpret_cast<f64x2*>(P + (i / RP) * LDP + i % RP) = src[i / 2];
+    }
     __syncthreads();
   };
   const int k0 = sp * r.len, k1 = min(max(r.rows, r.cols), k0 + r.len);
   const int64_t base = r.offset + mat * r.stride;
-  if (r.rows <= r.cols) apply_range<RP, true, VEC, MUON, 4>(p, r, P, base, k0, k1, sc, ready);
+  if (wide) apply_range<RP, true, VEC, MUON, 4>(p, r, P, base, k0, k1, sc, ready);
   else apply_range<RP, false, VEC, MUON, 4>(p, r, P, base, k0, k1, sc, ready);
 }
 
