@@ -19,9 +19,9 @@
 // usual a and five steps) where a singular value is small, and an error e of
 // G_0 there becomes P e X: with float32 sums of G a spectrum wider than 1e3
 // would lose all but three digits.  In float64 the results are as accurate as
-// the float32 data, and the two passes still cost less MFMA time than memory
-// time up to R = 128 (2 R flops an element each, the first half of that by
-// symmetry, at 64 flops a byte and more).  Measured for 72 x [9728, 64]: gram
+// the float32 data, and up to R = 64 the two passes still cost less MFMA time
+// (2 R flops an element in the second, 5/8 of that in the first by symmetry)
+// than memory time; at 128 about as much.  Measured for 72 x [9728, 64]: gram
 // 110 us (543 MB, 4.9 TB/s), poly 38, apply 155 (724 MB, 4.7 TB/s); wide
 // matrices, whose rows are read in 64-byte pieces, 20 % slower.
 //
