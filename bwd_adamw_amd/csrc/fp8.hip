@@ -16,17 +16,17 @@ namespace {
 // Tiles: tokens, columns, wave grid, stages in LDS (130, 66 and 63 KB of
 // them), blocks a CU holds, and the time of one contraction step of a CU's
 // resident blocks and of a block's ends, in microseconds, fitted to all three
-// on the Qwen3-4B-shaped products at 128 to 4096 tokens.  4096 tokens of
-// [2560 -> 4096] forward: 43, 56 and 96 us; 512 of them 34, 25 and 15; 1000
-// of [2056 -> 1368] 28, 23 and 12.
+// on the Qwen3-4B-shaped products at 512 to 4096 tokens.  4096 tokens of
+// [2560 -> 4096] forward: 71, 82 and 129 us; 512 of them 35, 29 and 19; 1000
+// of [2056 -> 1368] 30, 25 and 16.
 struct Fp8Cfg {
   int bm, bn, per_cu;
   double step, ends;
 };
 #define LORA_FP8_CFGS(X)                          \
-  X(0, 256, 256, 2, 4, 2, 1, 1.5, 13.0)           \
-  X(1, 128, 128, 2, 2, 2, 2, 0.95, 7.0)           \
-  X(2, 32, 128, 1, 4, 3, 2, 0.42, 5.0)
+  X(0, 256, 256, 2, 4, 2, 1, 2.9, 16.0)           \
+  X(1, 128, 128, 2, 2, 2, 2, 1.88, 4.5)           \
+  X(2, 32, 128, 1, 4, 3, 2, 0.73, 4.7)
 constexpr Fp8Cfg kCfg[] = {
 #define LORA_FP8_ROW(i, bm, bn, wm, wn, ns, pc, st, en) {bm, bn, pc, st, en},
     LORA_FP8_CFGS(LORA_FP8_ROW)
@@ -39,6 +39,10 @@ struct Fp8Plan {
   int cfg, per, nsplit;
   double t;          // microseconds
 };
+// Rounds of a CU's blocks: all but the first start under the last one's end.
+double round_time(const Fp8Cfg& c, int64_t rounds, int steps) {
+  return c.ends + rounds * (steps * c.step) + (rounds - 1) * 1.0;
+}
 // most: the largest number of splits.
 Fp8Plan plan(int64_t M, int64_t Nc, int nk, int most = 16) {
   Fp8Plan best = {0, nk, 1, 1e30};
@@ -48,8 +52,7 @@ Fp8Plan plan(int64_t M, int64_t Nc, int nk, int most = 16) {
     for (int want = 1; want <= std::min(nk, most); ++want) {
       const int per = (int)cdiv(nk, want), n = (int)cdiv(nk, per);
       if (n != want) continue;
-      const double rounds = (double)cdiv(tiles * n, kCUs * c.per_cu);
-      double t = rounds * (per * c.step + c.ends);
+      double t = round_time(c, cdiv(tiles * n, kCUs * c.per_cu), per);
       // Split partials: written, read, and summed by a launch of its own.
       if (n > 1) t += 2.5 + 4.0 * M * Nc * (1.6 * n) / 5e6;
       if (t < best.t) best = {i, per, n, t};
@@ -61,13 +64,13 @@ Fp8Plan plan(int64_t M, int64_t Nc, int nk, int most = 16) {
 // Columns that run first, as whole rounds of the largest tile, when the rest
 // in a launch of their own is faster than a last, partly filled round (4096
 // tokens of [2560 -> 9728]: two rounds and 1536 columns instead of three
-// rounds, 128 -> 117 us); 0: all in one.
+// rounds, 192 -> 173 us); 0: all in one.
 int64_t whole_rounds(const Fp8Plan& g, int64_t M, int64_t Nc, int nk) {
   const Fp8Cfg& c = kCfg[0];
   const int64_t ntm = cdiv(M, c.bm), full = ntm * cdiv(Nc, c.bn) / kCUs;
   const int64_t cols = full * kCUs / ntm * c.bn;
-  if (g.cfg != 0 || g.nsplit != 1 || full < 1 || cols >= Nc) return 0;
-  const double two = full * (nk * c.step + c.ends) + plan(M, Nc - cols, nk, 1).t + 3.0;
+  if (g.nsplit != 1 || full < 1 || cols >= Nc) return 0;
+  const double two = round_time(c, full, nk) + plan(M, Nc - cols, nk, 1).t + 3.0;
   return two < g.t ? cols : 0;
 }
 
@@ -91,9 +94,8 @@ int check_fp8(const lora_fp8_operand* x, int64_t N, int64_t K, int dx) {
 }
 
 // Few tokens, forward: up to one tile of 16 run without stages or splits, in
-// one launch.  One token of [2560 -> 4096]: 4.5 us against 7.6 of the 32-token
-// tiles and their sum; 16 tokens of [2560 -> 9728] 9.9 against 11.0; two such
-// tiles (32 tokens of [9728 -> 2560]) took 16.0 against 12.2.
+// one launch.  [2560 -> 9728]: 16 tokens 9.5 us, where 17 take 10.7 on the
+// 32-token tile with its split sums; one token 6.6.
 constexpr int64_t kFewTokens = 16;
 bool few(int64_t M, bool dx) { return !dx && M <= kFewTokens; }
 
@@ -265,7 +267,7 @@ int lora_fp8_product(const lora_fp8_operand* x, const void* W, int64_t out_dim, 
   if (first) {
     Fp8Args q = a;
     q.Nc = first;
-    product(q, g.cfg);
+    product(q, 0);
     q.Nc = a.Nc - first;
     q.W += dx ? first : first * a.ldw;
     q.S += dx ? first / 128 : first / 128 * a.lds_;

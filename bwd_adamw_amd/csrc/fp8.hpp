@@ -7,16 +7,16 @@
 // where b runs over the 128-wide blocks of the contraction, q and 2^e are the
 // activations' e4m3 values and scales (fp8_quant_kernel) and Wq, w those of
 // W, read in its own [N, K] layout in both directions.  All 128 products of a
-// block share both scales, so one v_mfma_scale_f32_16x16x128_f8f6f4 takes a
-// block of a 16 x 16 tile at once: the instruction multiplies by 2^e, and one
-// float32 FMA per result adds the block with W's scale.
+// block share both scales: four MFMAs sum a block of a 16 x 16 tile, and one
+// float32 FMA per result adds it with W's scale.
 //
-// Accuracy: the e4m3 products are exact, and blocks are added in float32; in
-// between, the matrix instruction aligns the 128 products of a block to
-// their largest and drops what lies about 2^-14 below it.  Measured against
-// exact sums that leaves 1.3e-5 of the result (normal data) to 2.6e-5
-// (columns of different size), in every 8-bit MFMA of this chip alike; the
-// rounding to e4m3 itself is 2^-4.  A bf16 result hides it (2^-8).
+// Accuracy: the values are widened to bf16, which holds every e4m3 value (and
+// its product with a power of two) exactly, and multiplied by bf16 MFMA, whose
+// products are exact and whose sums are float32.  The 8-bit MFMAs take half
+// the time (4096 tokens of [2560 -> 4096]: 43 us against 75), but each aligns
+// the products of a block to their largest and drops what lies about 2^-14
+// below it: a result off by 1.3e-5 to 2.6e-5 on ordinary data, and by all of it
+// where large products cancel.
 //
 // Tile: BM tokens x BN columns, contraction step 128 = one scale block.  Both
 // operands go to LDS by direct-to-LDS loads, NS stages deep, as rows of 128
@@ -30,11 +30,12 @@
 // column c in those rows.
 //
 // Rate: the 256 x 256 tile runs 4096 tokens of [2560 -> 4096], one full round,
-// at 2.0 PFLOP/s (43 us); a step takes 1.5 us against the 1.0 that its MFMAs
-// need at the 4.2 PFLOP/s they reach alone.  The rest is the FMAs (four
-// for each MFMA, half its time, on the vector unit beside it) and the barrier
-// of each step.  Rounding moves 4 + 1 bytes a value at 5 TB/s (4096 x 2560:
-// 10.5 us).
+// at 1.15 PFLOP/s (75 us), of [9728 -> 4096] at 1.38; a step takes 2.9 us
+// against the 2.2 that its MFMAs need at the 1.95 PFLOP/s they reach alone.  The
+// rest is the vector unit's work (192 widenings and 128 FMAs a wave and step
+// for 128 MFMAs, two thirds of their time beside them), of which each step's
+// start, W's widening, stands alone in all waves.  Rounding moves 4 + 1 bytes a
+// value at 5 TB/s (4096 x 2560: 10.5 us).
 #pragma once
 #include <utility>
 
@@ -69,15 +70,44 @@ LORA_HD inline int64_t fp8_scale_at(int64_t t) {
   return (t & ~(int64_t)127) + (t & 15) * 8 + ((t >> 4) & 7);
 }
 
-// The B operand's scale is byte SEL of eb.
-template <int SEL>
-LORA_DEV f32x4 mfma_fp8(i32x8 a, i32x8 b, int eb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0, 0, 0, 0}, 0, 0, 0, 127, SEL,
-                                                          eb);
+// The 32 values of a fragment times a power of two, as four bf16 operands:
+// e4m3 has four significant bits, bf16 eight.
+struct Wide {
+  bf16x8 k[4];
+};
+LORA_DEV Wide widen(i32x8 f, float p2) {
+  Wide o;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t v[4];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      v[2 * w] = __builtin_bit_cast(
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[2 * q + w], p2, false));
+      v[2 * w + 1] = __builtin_bit_cast(
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[2 * q + w], p2, true));
+    }
+    o.k[q] = __builtin_bit_cast(bf16x8, u32x4{v[0], v[1], v[2], v[3]});
+  }
+  return o;
 }
+LORA_DEV f32x4 mfma16x16x32_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// A token's scale 2^(e - 127) and W's: as much of the first as keeps every
+// value and product a normal number goes into the token's operand (2^-100 to
+// 2^100), the rest (1 for blocks of 1e-28 to 5e32) into the factor of the sum.
+struct TokenScale {
+  float x, sum;
+  LORA_DEV TokenScale(int e, float w) {
+    const int in = min(max(e, 27), 227);
+    x = __uint_as_float((uint32_t)in << 23);
+    sum = ldexpf(w, e - in);
+  }
+};
 template <int J>
-LORA_DEV f32x4 mfma_fp8_at(i32x8 a, i32x8 b, const u32x2& e) {
-  return mfma_fp8<J % 4>(a, b, (int)e[J / 4]);
+LORA_DEV TokenScale scale_at(const u32x2& ex, float w) {
+  return TokenScale((int)((ex[J / 4] >> (8 * (J % 4))) & 0xffu), w);
 }
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
@@ -152,7 +182,6 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)   // the host pass has no use for the body
   constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr int XB = BM * 128, WB = BN * 128, STAGE = XB + WB + 1024;   // X, W, exponents
-  constexpr bool MIX = TM == 4;
   constexpr int XL = XB / 1024 / NW, WL = WB / 1024 / NW;   // loads a wave and stage
   static_assert(XB % (1024 * NW) == 0 && WB % (1024 * NW) == 0, "whole loads per wave");
   static_assert(TM >= 1 && TN >= 1 && (BN / WN) <= 128 && 128 % (BN / WN) == 0, "one W scale a wave");
@@ -267,57 +296,36 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
     const lds_u8* X = lds + cur * STAGE + wm * 128;
     const lds_u8* W = lds + cur * STAGE + XB;
     const u32x2 ex = exponents(W + WB);
-    i32x8 wf[TN];
+    Wide w[TN];
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
       if constexpr (DX) {
         const int ch = (wn >> 4) + i;
-        wf[i] = frag_cols(W + wo[0] + 16 * ((ch & ~7) | ((ch ^ mrow) & 7)), BN);
+        w[i] = widen(frag_cols(W + wo[0] + 16 * ((ch & ~7) | ((ch ^ mrow) & 7)), BN), 1.0f);
       } else {
-        wf[i] = frag_rows(W + (wn + 16 * i) * 128, wo[0], wo[1]);
+        w[i] = widen(frag_rows(W + (wn + 16 * i) * 128, wo[0], wo[1]), 1.0f);
       }
     }
-    if constexpr (MIX) {
-      // Token tile J's MFMAs go out between the FMAs of tile J - 1, one with
-      // four FMAs each, and the reads of tile J + 1.  The 128-wide tile
-      // gains up to 9 % by it; the 256-wide one loses up to 10 % against the
-      // compiler's own order.
-      f32x4 d[2][TN];
-      i32x8 xf[2];
-      xf[0] = frag_rows(X, xo[0], xo[1]);
-      auto add = [&](auto J_) {
-        constexpr int J = decltype(J_)::value;
+    // A wave whose MFMAs are ready goes before one that widens: the two waves
+    // of a SIMD of the 256-wide tile part by it (dX of 4096 x [4096 -> 2560]:
+    // 80 -> 75 us).  The 128-wide tile's two blocks are apart already (82 -> 84).
+    unrolled<TM>([&](auto J_) {
+      constexpr int J = decltype(J_)::value;
+      const TokenScale ts = scale_at<J>(ex, sw);
+      const Wide x = widen(frag_rows(X + 16 * J * 128, xo[0], xo[1]), ts.x);
+      f32x4 d[TN];
+      if constexpr (TM == 8) __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int i = 0; i < TN; ++i)
+          d[i] = mfma16x16x32_bf16(w[i].k[q], x.k[q], q ? d[i] : f32x4{0, 0, 0, 0});
+      if constexpr (TM == 8) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][J][v] = fmaf(d[J & 1][i][v], sw, acc[i][J][v]);
-      };
-      unrolled<TM>([&](auto J_) {
-        constexpr int J = decltype(J_)::value;
-        if constexpr (J + 1 < TM) xf[(J + 1) & 1] = frag_rows(X + 16 * (J + 1) * 128, xo[0], xo[1]);
+      for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int i = 0; i < TN; ++i) d[J & 1][i] = mfma_fp8_at<J>(wf[i], xf[J & 1], ex);
-        if constexpr (J > 0) add(std::integral_constant<int, J - 1>{});
-#pragma unroll
-        for (int i = 0; i < TN; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          if constexpr (J > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-          if (i < 2 && J + 1 < TM) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-      });
-      add(std::integral_constant<int, TM - 1>{});
-    } else {
-      unrolled<TM>([&](auto J_) {
-        constexpr int J = decltype(J_)::value;
-        const i32x8 xf = frag_rows(X + 16 * J * 128, xo[0], xo[1]);
-#pragma unroll
-        for (int i = 0; i < TN; ++i) {
-          const f32x4 d = mfma_fp8_at<J>(wf[i], xf, ex);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][J][v] = fmaf(d[v], sw, acc[i][J][v]);
-        }
-      });
-    }
+        for (int v = 0; v < 4; ++v) acc[i][J][v] = fmaf(d[i][v], ts.sum, acc[i][J][v]);
+    });
     sw = wscale(k + 1);
     // Stage k + 1 is in once only the later stages' loads remain.
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * (XL + WL)) : "memory");
@@ -429,8 +437,8 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_gemm_kernel(Fp8Args p) {
 // block takes 16 columns; its eight waves take every eighth contraction step,
 // with the next two steps' fragments loading straight into registers, and
 // their sums meet in LDS in wave order.  W's rows are read in 64-byte pieces,
-// two of a step making whole lines.  One token of [2560 -> 4096]: 4.5 us for
-// 10.5 MB (2.3 TB/s, with the launch).
+// two of a step making whole lines.  One token of [2560 -> 4096]: 5.3 us for
+// 10.5 MB (2.0 TB/s, with the launch).
 template <bool BF16>
 __global__ __launch_bounds__(512) void fp8_few_kernel(Fp8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -465,9 +473,13 @@ __global__ __launch_bounds__(512) void fp8_few_kernel(Fp8Args p) {
                  (int)v[1][0], (int)v[1][1], (int)v[1][2], (int)v[1][3]};
   };
   auto add = [&](const Step& f) {
-    const f32x4 d = mfma_fp8<0>(frag(f.w), frag(f.x), f.e);
+    const TokenScale ts(f.e, f.s);
+    const Wide w = widen(frag(f.w), 1.0f), x = widen(frag(f.x), ts.x);
+    f32x4 d = {0, 0, 0, 0};
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[v] = fmaf(d[v], f.s, acc[v]);
+    for (int q = 0; q < 4; ++q) d = mfma16x16x32_bf16(w.k[q], x.k[q], d);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] = fmaf(d[v], ts.sum, acc[v]);
   };
   Step a, b, d;
   int k = wave;

@@ -37,7 +37,7 @@ inline bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // bf16 or block-quantized W: the frozen products run on bf16 MFMA.
 inline bool bf16_ops(int32_t w_dtype) { return w_dtype != LORA_F32 && w_dtype != LORA_FP8; }
-// 8-bit W: they run on 8-bit MFMA, over activations rounded to e4m3.
+// 8-bit W: they take activations rounded to e4m3 (fp8.hpp).
 inline bool fp8_ops(int32_t w_dtype) { return w_dtype == LORA_FP8; }
 
 // Planes of a block-quantized W [N, K] in one buffer: offset and size of

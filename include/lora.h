@@ -398,8 +398,8 @@ int lora_fp8_quantize(const void* X, int dtype, int64_t ldx, const lora_fp8_oper
 /* dx == 0: out [rows, out_dim] = x W^T, x [rows, in_dim] the rounded X;
  * dx != 0: out [rows, in_dim] = x W, x [rows, out_dim] the rounded dY.
  * out has type out_dtype, LORA_F32 or LORA_BF16 (rounded once, to nearest
- * even).  The products run on 8-bit MFMA: exact products, a block's 128 summed
- * to within 2^-14 of the largest, blocks summed in float32. */
+ * even).  The products are exact, a block's 128 are summed in float32, and so
+ * are the blocks with W's scales. */
 size_t lora_fp8_product_workspace_bytes(const lora_fp8_operand* x, int64_t out_dim, int64_t in_dim,
                                         int dx);
 int lora_fp8_product(const lora_fp8_operand* x, const void* W, int64_t out_dim, int64_t in_dim,
