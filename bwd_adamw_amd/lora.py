@@ -219,16 +219,17 @@ def _stream(stream):
 
 def _own_ws(need, device, stream):
     """A workspace from torch's allocator for a call on `stream` (None: the
-    current one).  The memory is this binding's to give back, when the call
-    returns: on another stream than the current one the allocator has to be
-    told that it is still in use there."""
-    ws = torch.empty(need, device=device, dtype=torch.uint8)
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
-                      else torch.cuda.default_stream(device))
-        ws.record_stream(stream)
-    return ws
+    current one), taken under that stream: what used the block before and what
+    gets it after the call returns is then ordered with the call's kernels.  A
+    block of the current stream's pool may still be in use by work queued there,
+    which a call on another stream does not wait for."""
+    if stream is None:
+        return torch.empty(need, device=device, dtype=torch.uint8)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return torch.empty(need, device=device, dtype=torch.uint8)
 
 
 def _check(fn, rc):
@@ -587,7 +588,7 @@ def lora_dora_row_norms(lin: LoraLinear, out_norm, ws=None, stream=None, split=T
     if ws is None and split:
         need = lora_dora_row_norms_workspace_bytes(lin)
         if need:
-            ws = torch.empty(need, device=out_norm.device, dtype=torch.uint8)
+            ws = _own_ws(need, out_norm.device, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     rc = lib().lora_dora_row_norms(C.byref(lin), _sized(out_norm, "out_norm", lin.out_dim),
                                    _ptr(ws, "ws", None), ws_bytes, _stream(stream))
@@ -607,7 +608,7 @@ def lora_dora_row_norms_batch(lins, out_norms, ws=None, stream=None):
     if ws is None:
         need = lora_dora_row_norms_batch_workspace_bytes(lins)
         if need:
-            ws = torch.empty(need, device=out_norms[0].device, dtype=torch.uint8)
+            ws = _own_ws(need, out_norms[0].device, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     rc = lib().lora_dora_row_norms_batch(len(lins), _linears(lins),
                                          _ptrs(out_norms, "out_norm", lins), _ptr(ws, "ws", None),
@@ -630,8 +631,7 @@ def lora_merge(lin: LoraLinear, W_out, rmse=None, ws=None, stream=None):
     else:
         raise TypeError(f"W_out must be float32 or bfloat16, got {W_out.dtype}")
     if rmse is not None and ws is None and od == BF16:
-        ws = torch.empty(max(8, lora_merge_workspace_bytes(lin)), device=W_out.device,
-                         dtype=torch.uint8)
+        ws = _own_ws(max(8, lora_merge_workspace_bytes(lin)), W_out.device, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     rc = lib().lora_merge(C.byref(lin), _sized(W_out, "W_out", lin.out_dim * lin.in_dim, None), od,
                           _sized(rmse, "rmse", 1, torch.float64), _ptr(ws, "ws", None), ws_bytes,
