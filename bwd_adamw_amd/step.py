@@ -22,7 +22,7 @@ linears' (layer, projection) order, so AdamW sees three segments.
 
 from __future__ import annotations
 
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 
 import torch
 
@@ -116,6 +116,19 @@ class Slot:
 
 
 @dataclass
+class _Norm:
+    """A norm before the groups that read its output."""
+    desc: L.LoraNorm
+    gamma: torch.Tensor | None
+    beta: torch.Tensor | None
+    X: torch.Tensor       # its output
+    stats: torch.Tensor
+    dH: torch.Tensor      # gradient of its input
+    groups: list = field(default_factory=list)
+    part: torch.Tensor | None = None   # dH of a further group
+
+
+@dataclass
 class StepStats:
     norm: float
     vetoed: bool
@@ -187,22 +200,29 @@ class Trainer:
             self.acts.append(a)
         self.U, self.Y, self.dX = (self.acts[0][n] for n in ("U", "Y", "dX"))
         # Norms before the groups: their output, row statistics and the
-        # gradient of their input, by the group's index.
-        self.norms = {}
+        # gradient of their input, by (layer, x_group); normed[gi] is group
+        # gi's.  Several groups can read one norm (more than MAX_GROUP
+        # projections of one X, or a group between them in key order).
+        self.norms, self.normed = {}, {}
         for gi, g in enumerate(self.groups):
-            nm = model.norms.get((g[0][0], xg[g[0][1]]))
-            if nm is None:
+            at = (g[0][0], xg[g[0][1]])
+            if at not in model.norms:
                 continue
             if self.stack_slots:
                 raise ValueError("norms before the groups need unstacked slots")
-            kind, eps, gamma, beta = nm
-            K = model.shape[g[0]][0]
-            desc = L.make_norm(kind, self.T, K, torch.float32, eps, gamma, beta)
-            self.norms[gi] = (desc, torch.empty(self.T, K, **f32), torch.empty(self.T, 2, **f32),
-                              torch.empty(self.T, K, **f32), (gamma, beta))
+            if at not in self.norms:
+                kind, eps, gamma, beta = model.norms[at]
+                K = model.shape[g[0]][0]
+                self.norms[at] = _Norm(L.make_norm(kind, self.T, K, torch.float32, eps, gamma, beta),
+                                       gamma, beta, torch.empty(self.T, K, **f32),
+                                       torch.empty(self.T, 2, **f32), torch.empty(self.T, K, **f32))
+            self.norms[at].groups.append(gi)
+            self.normed[gi] = self.norms[at]
+        for nm in self.norms.values():
+            if len(nm.groups) > 1:
+                nm.part = torch.empty_like(nm.dH)
         # dH[(layer, x_group)]: gradient of a norm's input after forward_backward
-        self.dH = {(self.groups[gi][0][0], xg[self.groups[gi][0][1]]): n[3]
-                   for gi, n in self.norms.items()}
+        self.dH = {at: nm.dH for at, nm in self.norms.items()}
         self.ws = torch.empty(max(ws, 256), device=device, dtype=torch.uint8)
         # Streams beyond the current one (default priority), each with a
         # workspace; no more streams than units to spread (layer groups; layers
@@ -212,6 +232,9 @@ class Trainer:
         self.side = [torch.cuda.Stream(device=device) for _ in range(nstreams - 1)]
         self.side_ws = [torch.empty(max(ws, 256), device=device, dtype=torch.uint8)
                         for _ in self.side]
+        # Stream of each group, round robin; the groups of one norm share one.
+        self._on = [(self.normed[gi].groups[0] if gi in self.normed else gi) % nstreams
+                    for gi in range(len(self.groups))]
         self._calls = {}   # (id(slot), group index) -> (slot, stream handle, norms, GroupCall)
         self._refresh = {}  # (streams, slot ids) -> (slots, [(stream, linears, norms)])
         self.d_scale = torch.zeros(1, **f32)
@@ -327,8 +350,7 @@ class Trainer:
         p = float(cfg.dropout)
         streams, wss = self._fork()
         ng = len(self.groups)
-        calls = [self._group_call(slot, gi, streams[gi % len(streams)], wss[gi % len(streams)])
-                 for gi in range(ng)]
+        calls = [self._group_call(slot, gi, streams[q], wss[q]) for gi, q in enumerate(self._on)]
         for g, chunk in enumerate(chunks):
             dr = [None] * ng
             if p > 0:
@@ -336,21 +358,25 @@ class Trainer:
                                           for k in keys])
                       for gi, keys in enumerate(self.groups)]
             for gi, keys in enumerate(self.groups):
-                X = chunk[keys[0]][0]
-                if gi in self.norms:
-                    desc, Xn, stats = self.norms[gi][:3]
-                    L.lora_norm_forward(desc, X, Xn, stats, stream=streams[gi % len(streams)])
-                    X = Xn
+                X, nm = chunk[keys[0]][0], self.normed.get(gi)
+                if nm is not None:
+                    if gi == nm.groups[0]:
+                        L.lora_norm_forward(nm.desc, X, nm.X, nm.stats, stream=streams[self._on[gi]])
+                    X = nm.X
                 calls[gi].forward(X, dr[gi])
             for gi in reversed(range(ng)):
-                keys = self.groups[gi]
-                X = self.norms[gi][1] if gi in self.norms else chunk[keys[0]][0]
+                keys, nm = self.groups[gi], self.normed.get(gi)
+                X = chunk[keys[0]][0] if nm is None else nm.X
                 calls[gi].backward(X, [chunk[k][1] for k in keys],
                                    accumulate=g > 0, drops=dr[gi])
-                if gi in self.norms:   # the group's gradients of X meet in the norm's backward
-                    desc, _, stats, dH = self.norms[gi][:4]
-                    L.lora_norm_backward(desc, chunk[keys[0]][0], [self.dX[k] for k in keys], stats,
-                                         dH, stream=streams[gi % len(streams)])
+                if nm is not None:   # the gradients of X meet in the norm's backward
+                    first, st = gi == nm.groups[-1], streams[self._on[gi]]
+                    L.lora_norm_backward(nm.desc, chunk[self.groups[nm.groups[0]][0]][0],
+                                         [self.dX[k] for k in keys], nm.stats,
+                                         nm.dH if first else nm.part, stream=st)
+                    if not first:   # linear in the gradients: the groups' results add up
+                        with torch.cuda.stream(st):
+                            nm.dH.add_(nm.part)
         self._join()
 
     def forward_backward_slots(self, slots: list, chunks_per_slot: list):
