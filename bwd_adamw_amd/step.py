@@ -156,10 +156,10 @@ class Trainer:
         self.T = cfg.tokens if tokens is None else int(tokens)
         # Slots over one W run their frozen products stacked (one pass over W
         # per product) when the library can: bf16 or quantized W and whole
-        # 256-row tiles.
+        # 256-row tiles.  Norms have one set of buffers: slots take turns.
         self.nslots = int(slots)
         self.stack_slots = (self.nslots > 1 and cfg.w_dtype not in ("f32", "fp8")
-                            and self.T % 256 == 0)
+                            and self.T % 256 == 0 and not model.norms)
         self.scale = L.lora_scaling(cfg.alpha, cfg.rank, cfg.scaling == "rslora")
         self.device = device
         f32 = dict(device=device, dtype=torch.float32)
@@ -208,8 +208,6 @@ class Trainer:
             at = (g[0][0], xg[g[0][1]])
             if at not in model.norms:
                 continue
-            if self.stack_slots:
-                raise ValueError("norms before the groups need unstacked slots")
             if at not in self.norms:
                 kind, eps, gamma, beta = model.norms[at]
                 K = model.shape[g[0]][0]
