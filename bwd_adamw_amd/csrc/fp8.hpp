@@ -157,7 +157,8 @@ LORA_DEV u32x4 row_bf16(const float* row, int64_t k, int64_t n, float mul) {
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const bool in = k + 4 * q < n;
-    v[q] = *reinterpret_cast<const f32x4*>(row + (in ? k + 4 * q : 0)) * (in ? mul : 0.0f);
+    const f32x4 x = *reinterpret_cast<const f32x4*>(row + (in ? k + 4 * q : 0)) * mul;
+    v[q] = in ? x : f32x4{0, 0, 0, 0};   // not a product with 0: x may be infinite
   }
   return u32x4{pack2(v[0][0], v[0][1]), pack2(v[0][2], v[0][3]), pack2(v[1][0], v[1][1]),
                pack2(v[1][2], v[1][3])};
