@@ -818,13 +818,16 @@ def _act(dtype) -> int:
 def make_norm(kind, rows, dim, dtype=torch.float32, eps=1e-5, gamma=None, beta=None, ldx=None,
               ldy=None) -> LoraNorm:
     """Descriptor of a row norm ("layer" or "rms") over X [rows, dim]; ldx and
-    ldy are the elements between rows of X, dX and of Y, dY (default dim)."""
+    ldy are the elements between rows of X, dX and of Y, dY (default dim).  The
+    descriptor keeps gamma and beta alive."""
     if kind not in NORM_KINDS:
         raise ValueError(f"norm kind must be one of {sorted(NORM_KINDS)}, got {kind!r}")
     dt = _act(dtype)
-    return LoraNorm(int(rows), int(dim), int(dim if ldx is None else ldx),
+    norm = LoraNorm(int(rows), int(dim), int(dim if ldx is None else ldx),
                     int(dim if ldy is None else ldy), NORM_KINDS[kind], dt,
                     _sized(gamma, "gamma", int(dim)), _sized(beta, "beta", int(dim)), float(eps))
+    norm.vectors = (gamma, beta)   # the structure itself holds only their addresses
+    return norm
 
 
 def _rows_ptr(t, name, rows, dim, ld, dtype):

@@ -119,8 +119,6 @@ class Slot:
 class _Norm:
     """A norm before the groups that read its output."""
     desc: L.LoraNorm
-    gamma: torch.Tensor | None
-    beta: torch.Tensor | None
     X: torch.Tensor       # its output
     stats: torch.Tensor
     dH: torch.Tensor      # gradient of its input
@@ -212,8 +210,8 @@ class Trainer:
                 kind, eps, gamma, beta = model.norms[at]
                 K = model.shape[g[0]][0]
                 self.norms[at] = _Norm(L.make_norm(kind, self.T, K, torch.float32, eps, gamma, beta),
-                                       gamma, beta, torch.empty(self.T, K, **f32),
-                                       torch.empty(self.T, 2, **f32), torch.empty(self.T, K, **f32))
+                                       torch.empty(self.T, K, **f32), torch.empty(self.T, 2, **f32),
+                                       torch.empty(self.T, K, **f32))
             self.norms[at].groups.append(gi)
             self.normed[gi] = self.norms[at]
         for nm in self.norms.values():
