@@ -110,7 +110,7 @@ bool plan_class(const lora_matrix_run* runs, int n, int rp, const lora_muon_hpar
   c.part = off;
   off += (size_t)rup(blk * tiles(rp) * 64 * 32, 256);
   c.poly = off;
-  off += (size_t)rup(mat * rp * rp * 8, 256);
+  if (rp > 16) off += (size_t)rup(mat * rp * rp * 8, 256);
   c.mem = off;
   if (rp == 128) off += (size_t)(mat * PolyMem<128>::BYTES);
   c.bytes = off;

@@ -60,7 +60,7 @@ struct MuonArgs {
   float* P;              // parameter arena, or the result of an orthogonalisation
   const float* d_scale;  // or NULL
   double* part;          // [block][tiles][64][4]
-  double* poly;          // [matrix][RP][RP]
+  double* poly;          // [matrix][RP][RP], RP above 16
   float mu;
   int nesterov;
   int steps;
@@ -358,15 +358,12 @@ struct PolyLds {
   f64x4 a[NM][F * F * 64];   // tile (w, t) at (w F + t) 64
   double diag[RP];
 };
-// Waves of poly_waves, and the barriers that they meet at.
+// Waves of poly_waves, and its barriers.
 template <int RP>
 constexpr int poly_nw() {
   return RP == 16 ? 1 : RP == 32 ? 4 : 8;   // RP up to 64
 }
-template <int RP>
-LORA_DEV int poly_syncs(int steps) {
-  return RP == 16 ? 2 : 1 + 3 * steps;
-}
+constexpr int POLY16_SYNCS = 2;   // at RP 16, for waves that only join them
 
 // s = the n values at `in`, stride apart, in order; eight loads at a time, all
 // of them unconditional (past the last one it is read again, and not added).
@@ -772,7 +769,7 @@ __global__ __launch_bounds__(256, muon_per_cu<RP>()) void muon_apply_kernel(Muon
       if (threadIdx.x < 64) {
         poly_waves<RP>(p, wide, in, r.splits, m, P, LDP, sync);
       } else {
-        for (int i = 0; i < poly_syncs<RP>(p.steps); ++i) sync();
+        for (int i = 0; i < POLY16_SYNCS; ++i) sync();
       }
     } else {
       typedef double f64x2 __attribute__((ext_vector_type(2)));
@@ -793,6 +790,7 @@ __global__ __launch_bounds__(256, muon_per_cu<RP>()) void muon_apply_kernel(Muon
 // instead of three, with its second pass over the matrix in the CU's reach.
 template <int RP, bool VEC, bool MUON>
 __global__ __launch_bounds__(1024) void muon_small_kernel(MuonArgs p) {
+  static_assert(RP == 16, "POLY16_SYNCS");
   constexpr int LDP = RP + 4, NT = muon_tiles<RP>();
   __shared__ f64x4 sum[NT * 64];
   __shared__ PolyLds<RP> m;
@@ -809,7 +807,7 @@ __global__ __launch_bounds__(1024) void muon_small_kernel(MuonArgs p) {
   if ((int)threadIdx.x < 64 * poly_nw<RP>()) {
     poly_waves<RP>(p, wide, sum, 1, m, P, LDP, sync);
   } else {
-    for (int i = 0; i < poly_syncs<RP>(p.steps); ++i) sync();
+    for (int i = 0; i < POLY16_SYNCS; ++i) sync();
   }
   __syncthreads();   // P, and the momentum that other waves wrote
   if (wide) apply_range<RP, true, VEC, MUON, 16>(p, r, P, base, 0, L, sc, [] {});
