@@ -1,5 +1,5 @@
-// Host-side helpers shared by the entry points that live outside
-// lora_api.hip: argument checks, sizes and the status of a launch.
+// Host-side helpers of the entry points: argument checks, sizes and the
+// status of a launch.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -19,6 +19,7 @@
 #include "gemm_bf16.hpp"
 #include "gemm_f32.hpp"
 #include "gemm_wq.hpp"
+#include "host.hpp"
 #include "launch.hpp"
 #include "normbatch.hpp"
 #include "optim.hpp"
@@ -26,15 +27,11 @@
 #include "skinny.hpp"
 
 using namespace lora;
+using namespace lora::host;
 
 namespace {
 
 // --------------------------------------------------------------- helpers ---
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline int64_t rup(int64_t a, int64_t b) { return cdiv(a, b) * b; }
-inline int64_t clampi(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : (x > hi ? hi : x); }
-inline bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 // bf16 or block-quantized W: the frozen products run on bf16 MFMA.
 inline bool bf16_ops(int32_t w_dtype) { return w_dtype != LORA_F32 && w_dtype != LORA_FP8; }
 // 8-bit W: they take activations rounded to e4m3 (fp8.hpp).
@@ -126,7 +123,6 @@ int64_t resident_per_cu(F kern) {
   }
   return n;
 }
-constexpr int64_t kCUs = 256;
 
 // Resident blocks of k4 on the whole chip, per padded rank; looked up once
 // per instance.  (k3 keeps its target of 512 blocks: measured on the
@@ -475,8 +471,6 @@ int check_linear(const lora_linear* L) {
   if (!std::isfinite(L->scale)) return LORA_E_INVALID;
   return LORA_OK;
 }
-
-int hip_status() { return hipGetLastError() == hipSuccess ? LORA_OK : LORA_E_HIP; }
 
 // ----------------------------------------------------------- launchers ---
 #define LORA_RP_DISPATCH_32(rp, call)                 \
