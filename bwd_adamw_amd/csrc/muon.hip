@@ -65,7 +65,7 @@ constexpr int64_t kMuonMinLen = 128;
 
 // Short sides up to 16 with long sides up to this run whole in one block: one
 // CU's float64 MFMA takes 3.3 us for each 1024 of them (both products), which
-// from about here on costs more than the two launches saved.
+// from about here on costs more than the launch saved.
 constexpr int64_t kMuonSmallLen = 512;
 
 bool plan_class(const lora_matrix_run* runs, int n, int rp, const lora_muon_hparams* h, Class& c) {

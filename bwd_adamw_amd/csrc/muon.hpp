@@ -787,7 +787,7 @@ __global__ __launch_bounds__(256, muon_per_cu<RP>()) void muon_apply_kernel(Muon
 }
 
 // All three steps of a small matrix in one block (sixteen waves): one launch
-// instead of three, with its second pass over the matrix in the CU's reach.
+// instead of two, with its second pass over the matrix in the CU's reach.
 template <int RP, bool VEC, bool MUON>
 __global__ __launch_bounds__(1024) void muon_small_kernel(MuonArgs p) {
   static_assert(RP == 16, "POLY16_SYNCS");

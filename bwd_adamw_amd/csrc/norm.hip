@@ -14,9 +14,13 @@ using namespace lora::host;
 
 namespace {
 
-// Lanes a row and 4-element groups a lane, by the width that they hold: the
-// fewest lanes with at most five groups each, so that the backward's five
-// arrays of them stay in registers beside the loads in flight.
+// Lanes a row and 4-element groups a lane, by the width that they hold: one
+// group a lane up to a wave's 256 elements, two or four in one wave up to 1024,
+// then three to five in two, four or eight waves, so that the backward's five
+// arrays of them stay in registers beside the loads in flight.  Past 10240
+// elements eight waves hold eight groups each, the most that a block takes: of
+// the backward's kernels those of four float32 gradients and of element loads
+// spill there (44 and 68 bytes a lane), none elsewhere.
 #define LORA_NORM_SHAPES(X) \
   X(16, 1) X(32, 1) X(64, 1) X(64, 2) X(64, 4) X(128, 3) X(128, 4) X(128, 5) X(256, 4) X(256, 5) \
   X(512, 4) X(512, 5) X(512, 8)
