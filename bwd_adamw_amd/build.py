@@ -18,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 SRCS = [os.path.join(CSRC, f) for f in
         ("lora_api.hip", "gemm_q8_0.hip", "gemm_q4_0.hip", "gemm_q4_k.hip", "gemm_q6_k.hip",
-         "norm.hip", "muon.hip", "fp8.hip")]
+         "norm.hip", "muon.hip", "fp8.hip", "heads.hip", "attention.hip")]
 OUT = os.path.join(HERE, "liblora.so")
 ARCH = "gfx950"
 

@@ -1,0 +1,163 @@
+// Entry points of the attention (include/lora.h: lora_attention_forward,
+// lora_attention_backward) and the choice of their kernels.
+#include <string.h>
+
+#include <cmath>
+
+#include "attention.hpp"
+#include "host.hpp"
+#include "launch.hpp"
+
+using namespace lora;
+using namespace lora::host;
+
+namespace {
+
+constexpr int64_t kMaxDim = 128, kMaxRows = (int64_t)1 << 31, kMaxLd = (int64_t)1 << 22;
+
+int64_t elem(int32_t dtype) { return dtype == LORA_F32 ? 4 : 2; }
+bool al_to(int64_t v, int64_t bytes) { return v * bytes % 16 == 0; }
+
+// Rows `ld` and heads `h` elements apart: one inside the other, no two
+// vectors of `dim` over one another.
+bool apart(int64_t tokens, int64_t heads, int64_t dim, int64_t ld, int64_t h) {
+  if (ld < dim || h < dim || ld > ((int64_t)1 << 40) || h > ((int64_t)1 << 40)) return false;
+  return ld >= (heads - 1) * h + dim || h >= (tokens - 1) * ld + dim;
+}
+
+int check_attn(const lora_attention* a) {
+  if (!a) return LORA_E_INVALID;
+  if (a->q_tokens <= 0 || a->k_tokens <= 0 || a->heads <= 0 || a->kv_heads <= 0 || a->seqs <= 0 ||
+      a->head_dim <= 0 || a->head_dim > kMaxDim || a->heads % a->kv_heads || a->seqs >= kMaxRows / 2 ||
+      a->heads >= 65536 || a->q_tokens >= kMaxRows / 2 / a->heads || a->k_tokens >= kMaxRows / 2 ||
+      a->seqs >= kMaxRows / 2 / a->heads)
+    return LORA_E_SHAPE;
+  if ((a->dtype != LORA_F32 && a->dtype != LORA_BF16) ||
+      (a->out_dtype != LORA_F32 && a->out_dtype != LORA_BF16) ||
+      (a->dtype == LORA_F32 && a->out_dtype != LORA_F32))
+    return LORA_E_DTYPE;
+  if (!apart(a->q_tokens, a->heads, a->head_dim, a->ldq, a->hq) ||
+      !apart(a->k_tokens, a->kv_heads, a->head_dim, a->ldk, a->hk) ||
+      !apart(a->k_tokens, a->kv_heads, a->head_dim, a->ldv, a->hv) ||
+      !apart(a->q_tokens, a->heads, a->head_dim, a->ldo, a->ho) || a->ldk > kMaxLd || a->ldv > kMaxLd)
+    return LORA_E_SHAPE;
+  if (!(a->scale > 0.0f) || !std::isfinite(a->scale) || !a->q_offsets || !a->k_offsets) return LORA_E_INVALID;
+  const int64_t e = elem(a->dtype), oe = elem(a->out_dtype);
+  if (a->head_dim % 8 || !al_to(a->ldq, e) || !al_to(a->hq, e) || !al_to(a->ldk, e) || !al_to(a->hk, e) ||
+      !al_to(a->ldv, e) || !al_to(a->hv, e) || !al_to(a->ldo, oe) || !al_to(a->ho, oe) ||
+      (((uintptr_t)a->q_offsets | (uintptr_t)a->k_offsets | (uintptr_t)a->k_lens) & 3u))
+    return LORA_E_ALIGN;
+  return LORA_OK;
+}
+
+AttnArgs attn_args(const lora_attention* a) {
+  AttnArgs p;
+  memset(&p, 0, sizeof(p));
+  p.qo = a->q_offsets;
+  p.ko = a->k_offsets;
+  p.kl = a->k_lens;
+  p.ldq = a->ldq, p.hq = a->hq, p.ldk = a->ldk, p.hk = a->hk;
+  p.ldv = a->ldv, p.hv = a->hv, p.ldo = a->ldo, p.ho = a->ho;
+  p.q_tokens = a->q_tokens;
+  p.k_tokens = a->k_tokens;
+  p.seqs = (int32_t)a->seqs;
+  p.kv = (int32_t)a->kv_heads;
+  p.group = (int32_t)(a->heads / a->kv_heads);
+  p.dim = (int32_t)a->head_dim;
+  p.causal = a->causal ? 1 : 0;
+  p.scale = a->scale;
+  p.c = a->scale * kLog2e;
+  return p;
+}
+
+// Tiles of B rows over the batch (attention.hpp: Rows).
+int64_t tile_count(int64_t tokens, int64_t mul, int64_t seqs, int64_t B) { return tokens * mul / B + seqs; }
+
+// Algorithmic work of one causal sequence of the whole batch's mean length.
+double attn_pairs(const lora_attention* a) {
+  const double q = (double)a->q_tokens / a->seqs, k = (double)a->k_tokens / a->seqs;
+  return a->seqs * a->heads * (a->causal && k >= q ? q * (k - q) + q * (q + 1) / 2 : q * k);
+}
+double attn_bytes(const lora_attention* a, int n) {
+  const double e = (double)elem(a->dtype), oe = (double)elem(a->out_dtype);
+  return a->head_dim * (a->q_tokens * a->heads * (e + n * oe) + a->k_tokens * a->kv_heads * (2 * e + (n > 1 ? 2 * oe : 0)));
+}
+
+template <typename T, typename OT, int DP>
+void forward(const lora_attention* a, AttnArgs p, hipStream_t st) {
+  constexpr int RW = 4, KT = sizeof(T) == 2 ? 2 : 1;
+  p.tiles = (int32_t)tile_count(a->q_tokens, p.group, a->seqs, 32 * RW);
+  prof::Scope ps("attn_fwd", a->q_tokens, a->k_tokens, a->heads, 4.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 1));
+  launch_n(attn_fwd_kernel<T, OT, DP, RW, KT>, dim3((unsigned)(p.tiles * p.kv)), 64 * RW, st, ps, p);
+}
+
+template <typename T, typename OT, int DP>
+void backward(const lora_attention* a, AttnArgs p, hipStream_t st) {
+  constexpr int W = 4;
+  {
+    p.tiles = (int32_t)tile_count(a->q_tokens, p.group, a->seqs, 32 * W);
+    prof::Scope ps("attn_dq", a->q_tokens, a->k_tokens, a->heads, 6.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 3));
+    launch_n(attn_dq_kernel<T, OT, DP, W>, dim3((unsigned)(p.tiles * p.kv)), 64 * W, st, ps, p);
+  }
+  p.tiles = (int32_t)tile_count(a->k_tokens, 1, a->seqs, 32 * W);
+  prof::Scope ps("attn_dkv", a->q_tokens, a->k_tokens, a->heads, 8.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 2));
+  launch_n(attn_dkv_kernel<T, OT, DP, W>, dim3((unsigned)(p.tiles * p.kv)), 64 * W, st, ps, p);
+}
+
+template <typename F>
+void by_type(const lora_attention* a, F f) {
+  const bool wide = a->head_dim > 64;
+  if (a->dtype == LORA_F32) return wide ? f(float{}, float{}, std::integral_constant<int, 128>{})
+                                        : f(float{}, float{}, std::integral_constant<int, 64>{});
+  if (a->out_dtype == LORA_F32) return wide ? f(uint16_t{}, float{}, std::integral_constant<int, 128>{})
+                                            : f(uint16_t{}, float{}, std::integral_constant<int, 64>{});
+  return wide ? f(uint16_t{}, uint16_t{}, std::integral_constant<int, 128>{})
+              : f(uint16_t{}, uint16_t{}, std::integral_constant<int, 64>{});
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_attention_workspace_bytes(const lora_attention* at, int backward_) {
+  if (check_attn(at) != LORA_OK) return 0;
+  return backward_ ? (size_t)rup(at->heads * at->q_tokens * 4, 16) : 0;
+}
+
+int lora_attention_forward(const lora_attention* at, const void* Q, const void* K, const void* V, void* O, float* lse,
+                           void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_attn(at);
+  if (rc) return rc;
+  if (!Q || !K || !V || !O) return LORA_E_INVALID;
+  if (!al16(Q) || !al16(K) || !al16(V) || !al16(O) || ((uintptr_t)lse & 3u)) return LORA_E_ALIGN;
+  const size_t need = lora_attention_workspace_bytes(at, 0);
+  if (need && (!ws || ws_bytes < need || !al16(ws))) return LORA_E_WORKSPACE;
+  AttnArgs p = attn_args(at);
+  p.Q = Q, p.K = K, p.V = V, p.O = O, p.lse = lse;
+  by_type(at, [&](auto t, auto o, auto d) {
+    forward<decltype(t), decltype(o), decltype(d)::value>(at, p, (hipStream_t)stream);
+  });
+  return hip_status();
+}
+
+int lora_attention_backward(const lora_attention* at, const void* Q, const void* K, const void* V, const void* O,
+                            const void* dO, const float* lse, void* dQ, void* dK, void* dV, void* ws, size_t ws_bytes,
+                            void* stream) {
+  const int rc = check_attn(at);
+  if (rc) return rc;
+  if (!Q || !K || !V || !O || !dO || !lse || !dQ || !dK || !dV) return LORA_E_INVALID;
+  if (!al16(Q) || !al16(K) || !al16(V) || !al16(O) || !al16(dO) || !al16(dQ) || !al16(dK) || !al16(dV) ||
+      ((uintptr_t)lse & 3u))
+    return LORA_E_ALIGN;
+  const size_t need = lora_attention_workspace_bytes(at, 1);
+  if (!ws || ws_bytes < need || !al16(ws)) return LORA_E_WORKSPACE;
+  AttnArgs p = attn_args(at);
+  p.Q = Q, p.K = K, p.V = V, p.O = const_cast<void*>(O), p.dO = dO, p.lse = const_cast<float*>(lse);
+  p.dQ = dQ, p.dK = dK, p.dV = dV, p.delta = (float*)ws;
+  by_type(at, [&](auto t, auto o, auto d) {
+    backward<decltype(t), decltype(o), decltype(d)::value>(at, p, (hipStream_t)stream);
+  });
+  return hip_status();
+}
+
+}  // extern "C"

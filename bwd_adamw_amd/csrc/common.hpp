@@ -62,6 +62,34 @@ LORA_DEV uint32_t pack_bf16x2(float lo, float hi) {
 }
 LORA_DEV float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
+// Elements of float32 or bf16 (uint16_t) memory as float32, one or four at a time.
+template <typename T>
+LORA_DEV float load1(const T* p) {
+  if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float*>(p);
+  else return bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(p));
+}
+template <typename T>
+LORA_DEV f32x4 load4(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const f32x4*>(p);
+  } else {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+    return f32x4{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u),
+                 __uint_as_float(v[1] << 16), __uint_as_float(v[1] & 0xffff0000u)};
+  }
+}
+// Float32 as it is, bf16 rounded to nearest even: the one rounding of the result.
+template <typename T>
+LORA_DEV void store1(T* p, float v) {
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<float*>(p) = v;
+  else *reinterpret_cast<uint16_t*>(p) = (uint16_t)f32_to_bf16_bits(v);
+}
+template <typename T>
+LORA_DEV void store4(T* p, f32x4 v) {
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4*>(p) = v;
+  else *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
 // ---------------------------------------------------------------------------
 // MFMA wrappers.  Operand/result lane layouts (wave64):
 //  32x32x2 f32 : a = A[l%32][l/32], b = B[l/32][l%32],

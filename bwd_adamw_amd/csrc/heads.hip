@@ -1,0 +1,206 @@
+// Entry points of the head norm and rotation (include/lora.h:
+// lora_heads_forward, lora_heads_backward).
+#include <string.h>
+
+#include <cmath>
+
+#include "heads.hpp"
+#include "host.hpp"
+#include "launch.hpp"
+
+using namespace lora;
+using namespace lora::host;
+
+namespace {
+
+constexpr int64_t kMaxHeadDim = 256, kMost = (int64_t)1 << 30, kMostLd = (int64_t)1 << 40;
+
+int check_one(const lora_heads& h) {
+  if (h.tokens <= 0 || h.heads <= 0 || h.head_dim <= 0 || h.head_dim > kMaxHeadDim || h.tokens > kMost ||
+      h.heads > 65536 || h.rot_dim < 0 || h.rot_dim > h.head_dim || h.rot_dim % 2)
+    return LORA_E_SHAPE;
+  for (const auto& [ld, hd] : {std::pair{h.ldx, h.hx}, {h.ldy, h.hy}}) {
+    if (ld < h.head_dim || hd < h.head_dim || ld > kMostLd || hd > kMostLd) return LORA_E_SHAPE;
+    if (ld < (h.heads - 1) * hd + h.head_dim && hd < (h.tokens - 1) * ld + h.head_dim) return LORA_E_SHAPE;
+  }
+  if ((h.x_dtype != LORA_F32 && h.x_dtype != LORA_BF16) || (h.y_dtype != LORA_F32 && h.y_dtype != LORA_BF16))
+    return LORA_E_DTYPE;
+  if (!(h.eps >= 0.0f) || !std::isfinite(h.eps)) return LORA_E_INVALID;
+  if ((h.rot_dim && !h.freqs) || (!h.norm && h.gamma)) return LORA_E_INVALID;
+  if (((uintptr_t)h.gamma & 3u) || ((uintptr_t)h.freqs & 7u)) return LORA_E_ALIGN;
+  return LORA_OK;
+}
+int check_heads(int n, const lora_heads* h) {
+  if (n < 1 || n > LORA_MAX_GROUP || !h) return LORA_E_INVALID;
+  for (int i = 0; i < n; ++i) {
+    const int rc = check_one(h[i]);
+    if (rc) return rc;
+    if (h[i].tokens != h[0].tokens) return LORA_E_SHAPE;
+  }
+  return LORA_OK;
+}
+
+int64_t size_of(int32_t dtype) { return dtype == LORA_F32 ? 4 : 2; }
+bool al_elem(const void* p, int32_t dtype) { return ((uintptr_t)p & (uintptr_t)(size_of(dtype) - 1)) == 0; }
+// Four values at a time (16 bytes of float32, 8 of bf16).
+bool vec4(const void* p, int32_t dtype, int64_t ld, int64_t h) {
+  return ((uintptr_t)p & (uintptr_t)(4 * size_of(dtype) - 1)) == 0 && ld % 4 == 0 && h % 4 == 0;
+}
+
+int lanes_of(int n, const lora_heads* h) {   // lanes a head, eight values each
+  int64_t dim = 0;
+  for (int i = 0; i < n; ++i) dim = h[i].head_dim > dim ? h[i].head_dim : dim;
+  return dim <= 32 ? 4 : dim <= 64 ? 8 : dim <= 128 ? 16 : 32;
+}
+
+// Ranges of a token's heads: one, unless that leaves most of the chip idle.
+void split_heads(const lora_heads& h, int lph, HeadsOne& d) {
+  const int64_t steps = cdiv(h.heads, 64 / lph);
+  const int64_t ranges = clampi(cdiv(16 * kCUs, h.tokens), 1, steps);
+  d.iters = (int32_t)cdiv(steps, ranges);
+  d.ranges = (int32_t)cdiv(steps, d.iters);
+}
+// Blocks of four waves: at most `cap` for one of the sets.
+int64_t heads_blocks(int n, const lora_heads* h, int64_t cap) {
+  int64_t most = 1;
+  for (int i = 0; i < n; ++i) {
+    HeadsOne d;
+    split_heads(h[i], lanes_of(n, h), d);
+    most = clampi(cdiv(h[i].tokens * d.ranges, 4), most, cap);
+  }
+  return most;
+}
+// Forward: any number.  Backward: two a CU, each of which leaves a partial of
+// dgamma.
+constexpr int64_t kFwd = 16 * kCUs, kBwd = 2 * kCUs;
+
+HeadsArgs heads_args(int n, const lora_heads* h, const int32_t* pos) {
+  HeadsArgs a;
+  memset(&a, 0, sizeof(a));
+  a.pos = pos;
+  a.tokens = h[0].tokens;
+  for (int i = 0; i < n; ++i) {
+    HeadsOne& d = a.one[i];
+    d.gamma = h[i].gamma;
+    d.freqs = h[i].freqs;
+    d.ldx = h[i].ldx, d.hx = h[i].hx, d.ldy = h[i].ldy, d.hy = h[i].hy;
+    d.heads = (int32_t)h[i].heads;
+    d.dim = (int32_t)h[i].head_dim;
+    d.rot = (int32_t)h[i].rot_dim;
+    d.norm = h[i].norm ? 1 : 0;
+    d.inter = h[i].interleaved ? 1 : 0;
+    d.xbf = h[i].x_dtype == LORA_BF16;
+    d.ybf = h[i].y_dtype == LORA_BF16;
+    d.eps = h[i].eps;
+    d.fdim = (float)h[i].head_dim;
+    split_heads(h[i], lanes_of(n, h), d);
+  }
+  return a;
+}
+bool vec_dims(const lora_heads& h) { return h.head_dim % 8 == 0 && h.rot_dim % 8 == 0; }
+
+template <bool FWD, bool VEC>
+void launch_heads(int lph, const HeadsArgs& a, dim3 grid, hipStream_t st, const prof::Scope& ps) {
+#define LORA_HEADS(L_)                                                                  \
+  if (lph == L_) {                                                                      \
+    if constexpr (FWD) launch(heads_fwd_kernel<L_, VEC>, grid, st, ps, a);              \
+    else launch(heads_bwd_kernel<L_, VEC>, grid, st, ps, a);                            \
+    return;                                                                             \
+  }
+  LORA_HEADS(4) LORA_HEADS(8) LORA_HEADS(16) LORA_HEADS(32)
+#undef LORA_HEADS
+}
+
+}  // namespace
+
+extern "C" {
+
+int lora_heads_forward(int n, const lora_heads* heads, const void* const* X, void* const* Y,
+                       const int32_t* positions, void* stream) {
+  const int rc = check_heads(n, heads);
+  if (rc) return rc;
+  if (!X || !Y) return LORA_E_INVALID;
+  HeadsArgs a = heads_args(n, heads, positions);
+  bool vec = true;
+  double flops = 0, bytes = 0;
+  for (int i = 0; i < n; ++i) {
+    const lora_heads& h = heads[i];
+    if (!X[i] || !Y[i] || (h.rot_dim && !positions)) return LORA_E_INVALID;
+    if (!al_elem(X[i], h.x_dtype) || !al_elem(Y[i], h.y_dtype)) return LORA_E_ALIGN;
+    a.one[i].X = X[i];
+    a.one[i].out = Y[i];
+    vec = vec && vec_dims(h) && vec4(X[i], h.x_dtype, h.ldx, h.hx) && vec4(Y[i], h.y_dtype, h.ldy, h.hy);
+    const double e = (double)h.tokens * h.heads * h.head_dim;
+    flops += 8 * e;
+    bytes += e * (size_of(h.x_dtype) + size_of(h.y_dtype));
+  }
+  if ((uintptr_t)positions & 3u) return LORA_E_ALIGN;
+  prof::Scope ps("heads_fwd", heads->tokens, heads->heads * heads->head_dim, n, flops, bytes);
+  const dim3 grid((unsigned)heads_blocks(n, heads, kFwd), (unsigned)n);
+  const int lph = lanes_of(n, heads);
+  if (vec) launch_heads<true, true>(lph, a, grid, (hipStream_t)stream, ps);
+  else launch_heads<true, false>(lph, a, grid, (hipStream_t)stream, ps);
+  return hip_status();
+}
+
+size_t lora_heads_workspace_bytes(int n, const lora_heads* heads) {
+  if (check_heads(n, heads) != LORA_OK) return 0;
+  const int64_t blocks = heads_blocks(n, heads, kBwd);
+  int64_t dims = 0;
+  for (int i = 0; i < n; ++i) dims += heads[i].norm ? heads[i].head_dim : 0;
+  return blocks > 1 ? (size_t)(blocks * dims) * sizeof(float) : 0;
+}
+
+int lora_heads_backward(int n, const lora_heads* heads, const void* const* X, const void* const* dY, void* const* dX,
+                        float* const* dgamma, const int32_t* positions, int accumulate, void* ws, size_t ws_bytes,
+                        void* stream) {
+  const int rc = check_heads(n, heads);
+  if (rc) return rc;
+  if (!dY) return LORA_E_INVALID;
+  HeadsArgs a = heads_args(n, heads, positions);
+  a.accumulate = accumulate ? 1 : 0;
+  const int64_t blocks = heads_blocks(n, heads, kBwd);
+  bool vec = true, sums = false;
+  int64_t widest = 0, off = 0;
+  double flops = 0, bytes = 0;
+  for (int i = 0; i < n; ++i) {
+    const lora_heads& h = heads[i];
+    HeadsOne& d = a.one[i];
+    d.X = X ? X[i] : nullptr;
+    d.dY = dY[i];
+    d.out = dX ? dX[i] : nullptr;
+    d.dgamma = dgamma ? dgamma[i] : nullptr;
+    if (!d.dY || (h.rot_dim && !positions) || (h.norm && !d.X) || (!d.out && !d.dgamma) || (d.dgamma && !h.norm))
+      return LORA_E_INVALID;
+    if (!al_elem(d.X, h.x_dtype) || !al_elem(d.out, h.x_dtype) || !al_elem(d.dY, h.y_dtype) ||
+        ((uintptr_t)d.dgamma & 3u))
+      return LORA_E_ALIGN;
+    vec = vec && vec_dims(h) && vec4(d.X, h.x_dtype, h.ldx, h.hx) && vec4(d.out, h.x_dtype, h.ldx, h.hx) &&
+          vec4(d.dY, h.y_dtype, h.ldy, h.hy);
+    d.part = (float*)ws + off;
+    off += h.norm ? blocks * h.head_dim : 0;
+    sums = sums || d.dgamma;
+    widest = h.head_dim > widest ? h.head_dim : widest;
+    const double e = (double)h.tokens * h.heads * h.head_dim;
+    flops += 16 * e;
+    bytes += e * (size_of(h.x_dtype) * ((h.norm ? 1 : 0) + (d.out ? 1 : 0)) + size_of(h.y_dtype));
+  }
+  if ((uintptr_t)positions & 3u) return LORA_E_ALIGN;
+  const size_t need = sums ? lora_heads_workspace_bytes(n, heads) : 0;
+  if (need && (!ws || ws_bytes < need || !al16(ws))) return LORA_E_WORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  {
+    prof::Scope ps("heads_bwd", heads->tokens, heads->heads * heads->head_dim, n, flops, bytes);
+    const dim3 grid((unsigned)blocks, (unsigned)n);
+    const int lph = lanes_of(n, heads);
+    if (vec) launch_heads<false, true>(lph, a, grid, st, ps);
+    else launch_heads<false, false>(lph, a, grid, st, ps);
+  }
+  if (sums && blocks > 1) {
+    prof::Scope ps("heads_finish", blocks, widest, n, 0.0, 4.0 * off);
+    launch_n(heads_finish_kernel, dim3((unsigned)cdiv(widest, 32), (unsigned)n), 1024u, st, ps, a, (int)blocks);
+  }
+  return hip_status();
+}
+
+}  // extern "C"

@@ -50,33 +50,6 @@ struct NormArgs {
   float eps, fdim;
 };
 
-template <typename T>
-LORA_DEV float load1(const T* p) {
-  if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float*>(p);
-  else return bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(p));
-}
-template <typename T>
-LORA_DEV f32x4 load4(const T* p) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const f32x4*>(p);
-  } else {
-    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-    return f32x4{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u),
-                 __uint_as_float(v[1] << 16), __uint_as_float(v[1] & 0xffff0000u)};
-  }
-}
-// Float32 as it is, bf16 rounded to nearest even: the one rounding of the result.
-template <typename T>
-LORA_DEV void store1(T* p, float v) {
-  if constexpr (sizeof(T) == 4) *reinterpret_cast<float*>(p) = v;
-  else *reinterpret_cast<uint16_t*>(p) = (uint16_t)f32_to_bf16_bits(v);
-}
-template <typename T>
-LORA_DEV void store4(T* p, f32x4 v) {
-  if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4*>(p) = v;
-  else *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-}
-
 constexpr int norm_threads(int tpr) { return tpr > 256 ? tpr : 256; }
 
 // Sum of a and b over the TPR lanes of a row; every lane gets both.  `buf`

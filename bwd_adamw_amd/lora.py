@@ -33,6 +33,9 @@ __all__ = [
     "Fp8Weight", "fp8_pack", "Fp8Rows", "fp8_rows", "lora_fp8_weight_layout",
     "lora_fp8_operand_layout", "lora_fp8_quantize", "lora_fp8_product_workspace_bytes",
     "lora_fp8_product",
+    "LoraHeads", "make_heads", "rope_freqs", "lora_heads_forward", "lora_heads_workspace_bytes",
+    "lora_heads_backward", "LoraAttention", "make_attention", "lora_attention_workspace_bytes",
+    "lora_attention_forward", "lora_attention_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblora.so")
@@ -59,6 +62,8 @@ EXPORTS = (
     "lora_muon_workspace_bytes", "lora_orthogonalize", "lora_muon_step",
     "lora_fp8_weight_layout", "lora_fp8_operand_layout", "lora_fp8_quantize",
     "lora_fp8_product_workspace_bytes", "lora_fp8_product",
+    "lora_heads_forward", "lora_heads_workspace_bytes", "lora_heads_backward",
+    "lora_attention_workspace_bytes", "lora_attention_forward", "lora_attention_backward",
 )
 
 
@@ -100,6 +105,24 @@ class LoraNorm(C.Structure):
     _fields_ = [("rows", C.c_int64), ("dim", C.c_int64), ("ldx", C.c_int64), ("ldy", C.c_int64),
                 ("kind", C.c_int32), ("dtype", C.c_int32), ("gamma", C.c_void_p),
                 ("beta", C.c_void_p), ("eps", C.c_float)]
+
+
+class LoraHeads(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("heads", C.c_int64), ("head_dim", C.c_int64),
+                ("rot_dim", C.c_int64), ("ldx", C.c_int64), ("hx", C.c_int64), ("ldy", C.c_int64),
+                ("hy", C.c_int64), ("x_dtype", C.c_int32), ("y_dtype", C.c_int32),
+                ("norm", C.c_int32), ("interleaved", C.c_int32), ("gamma", C.c_void_p),
+                ("freqs", C.c_void_p), ("eps", C.c_float)]
+
+
+class LoraAttention(C.Structure):
+    _fields_ = [("q_tokens", C.c_int64), ("k_tokens", C.c_int64), ("heads", C.c_int64),
+                ("kv_heads", C.c_int64), ("head_dim", C.c_int64), ("seqs", C.c_int64),
+                ("ldq", C.c_int64), ("hq", C.c_int64), ("ldk", C.c_int64), ("hk", C.c_int64),
+                ("ldv", C.c_int64), ("hv", C.c_int64), ("ldo", C.c_int64), ("ho", C.c_int64),
+                ("dtype", C.c_int32), ("out_dtype", C.c_int32), ("causal", C.c_int32),
+                ("scale", C.c_float), ("q_offsets", C.c_void_p), ("k_offsets", C.c_void_p),
+                ("k_lens", C.c_void_p)]
 
 
 class LoraFp8Operand(C.Structure):
@@ -168,6 +191,12 @@ def lib() -> C.CDLL:
             "lora_norm_forward": (I32, [P, P, P, P, P]),
             "lora_norm_workspace_bytes": (SZ, [P]),
             "lora_norm_backward": (I32, [P, P, I32, P, P, P, P, P, I32, P, SZ, P]),
+            "lora_heads_forward": (I32, [I32, P, P, P, P, P]),
+            "lora_heads_workspace_bytes": (SZ, [I32, P]),
+            "lora_heads_backward": (I32, [I32, P, P, P, P, P, P, I32, P, SZ, P]),
+            "lora_attention_workspace_bytes": (SZ, [P, I32]),
+            "lora_attention_forward": (I32, [P, P, P, P, P, P, P, SZ, P]),
+            "lora_attention_backward": (I32, [P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -883,6 +912,168 @@ def lora_norm_backward(norm: LoraNorm, X, dY, stats, dX=None, dgamma=None, dbeta
                                   1 if accumulate else 0, _ptr(ws, "ws", None), ws_bytes,
                                   _stream(stream))
     _check("lora_norm_backward", rc)
+
+
+# ------------------------------------------------------ heads and attention
+def rope_freqs(rot_dim, base=10000.0, device="cuda"):
+    """base^(-2i/rot_dim) for the pairs i < rot_dim / 2, in float64: radians a
+    position."""
+    i = torch.arange(0, int(rot_dim), 2, dtype=torch.float64)
+    return (float(base) ** (-i / int(rot_dim))).to(device)
+
+
+def _device_ints(t, name, need):
+    return _sized(t, name, need, torch.int32)
+
+
+def make_heads(tokens, heads, head_dim, x_dtype=torch.float32, y_dtype=None, norm=True, eps=1e-6, gamma=None,
+               rot_dim=None, freqs=None, interleaved=False, ldx=None, hx=None, ldy=None,
+               hy=None) -> LoraHeads:
+    """Descriptor of a set of heads: norm (RMS over the head; gamma None: ones)
+    and rotation by `freqs` [rot_dim / 2] float64 (rope_freqs; None: no
+    rotation).  ldx and hx (X, dX), ldy and hy (Y, dY) are the elements between
+    tokens and between heads, by default those of [tokens, heads, head_dim].
+    y_dtype (default x_dtype) is the type of Y and of dY.  The descriptor keeps
+    gamma and freqs alive."""
+    rot = (0 if freqs is None else 2 * freqs.numel()) if rot_dim is None else int(rot_dim)
+    t, h, d = int(tokens), int(heads), int(head_dim)
+    hx, hy = int(d if hx is None else hx), int(d if hy is None else hy)
+    ldx, ldy = int(h * d if ldx is None else ldx), int(h * d if ldy is None else ldy)
+    out = LoraHeads(t, h, d, rot, ldx, hx, ldy, hy, _act(x_dtype), _act(y_dtype or x_dtype),
+                    1 if norm else 0, 1 if interleaved else 0, _sized(gamma, "gamma", d),
+                    _sized(freqs, "freqs", rot // 2, torch.float64), float(eps))
+    out.vectors = (gamma, freqs)
+    return out
+
+
+def _strided(t, name, tokens, heads, dim, ld, h, dtype):
+    """Device pointer of heads whose tokens are ld and heads h elements apart:
+    a [tokens, heads, dim] tensor of those strides, or (where the heads of a
+    token lie together) [tokens, heads * dim]."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if _act(t.dtype) != dtype:
+        raise TypeError(f"{name} must be {'float32' if dtype == F32 else 'bfloat16'}, got {t.dtype}")
+    if t.dim() == 2 and tuple(t.shape) == (tokens, heads * dim) and (h == dim or heads == 1):
+        shape, want = (tokens, heads * dim), (ld, 1)
+    else:
+        shape, want = (tokens, heads, dim), (ld, h, 1)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}], got {list(t.shape)}")
+    if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), want)):
+        raise ValueError(f"{name} must have strides {list(want)}, got {list(t.stride())}")
+    return t.data_ptr()
+
+
+def _head_ptrs(heads, ts, name, side):
+    if ts is None:
+        return None
+    if len(ts) != len(heads):
+        raise ValueError(f"{name} has {len(ts)} entries for {len(heads)} sets of heads")
+    return (C.c_void_p * len(ts))(*[
+        _strided(t, f"{name}[{i}]", h.tokens, h.heads, h.head_dim,
+                 *((h.ldx, h.hx, h.x_dtype) if side == "x" else (h.ldy, h.hy, h.y_dtype)))
+        for i, (t, h) in enumerate(zip(ts, heads))])
+
+
+def lora_heads_forward(heads, X, Y, positions=None, stream=None):
+    """Y[i] = the heads X[i], normed and rotated, for each set of `heads` (one
+    to four of the same tokens); positions [tokens] int32."""
+    arr = (LoraHeads * len(heads))(*heads)
+    rc = lib().lora_heads_forward(len(heads), arr, _head_ptrs(heads, X, "X", "x"), _head_ptrs(heads, Y, "Y", "y"),
+                                  _device_ints(positions, "positions", heads[0].tokens if len(heads) else 0),
+                                  _stream(stream))
+    _check("lora_heads_forward", rc)
+
+
+def lora_heads_workspace_bytes(heads) -> int:
+    return int(lib().lora_heads_workspace_bytes(len(heads), (LoraHeads * len(heads))(*heads)))
+
+
+def lora_heads_backward(heads, X, dY, dX=None, dgamma=None, positions=None, accumulate=False, ws=None,
+                        stream=None):
+    """Gradients of lora_heads_forward; dX and dgamma are lists (entries may be
+    None).  `ws` is taken from torch's allocator when a dgamma is wanted and it
+    is None."""
+    arr = (LoraHeads * len(heads))(*heads)
+    if dgamma is not None and len(dgamma) != len(heads):
+        raise ValueError(f"dgamma has {len(dgamma)} entries for {len(heads)} sets of heads")
+    dg = None if dgamma is None else (C.c_void_p * len(heads))(
+        *[_sized(t, f"dgamma[{i}]", h.head_dim) for i, (t, h) in enumerate(zip(dgamma, heads))])
+    if ws is None and dgamma is not None and any(t is not None for t in dgamma):
+        need = int(lib().lora_heads_workspace_bytes(len(heads), arr))
+        if need:
+            ws = _own_ws(need, dY[0].device, stream)
+    rc = lib().lora_heads_backward(len(heads), arr, _head_ptrs(heads, X, "X", "x"), _head_ptrs(heads, dY, "dY", "y"),
+                                   _head_ptrs(heads, dX, "dX", "x"), dg,
+                                   _device_ints(positions, "positions", heads[0].tokens if len(heads) else 0),
+                                   1 if accumulate else 0, _ptr(ws, "ws", None),
+                                   0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _check("lora_heads_backward", rc)
+
+
+def make_attention(q_tokens, k_tokens, heads, kv_heads, head_dim, q_offsets, k_offsets, k_lens=None,
+                   dtype=torch.bfloat16, out_dtype=None, scale=None, causal=True, q_strides=None, k_strides=None,
+                   v_strides=None, o_strides=None) -> LoraAttention:
+    """Descriptor of attention over the packed sequences of q_offsets and
+    k_offsets [sequences + 1] (k_lens [sequences]: the keys in use of each
+    sequence's room), int32 on the GPU.  Strides are (elements between tokens,
+    between heads), by default those of [tokens, heads, head_dim].  out_dtype
+    (default dtype) is the type of O and of all gradients; scale defaults to
+    head_dim^-1/2.  The descriptor keeps the offsets alive."""
+    d, seqs = int(head_dim), int(q_offsets.numel()) - 1
+    st = lambda given, n: (int(n) * d, d) if given is None else tuple(map(int, given))
+    at = LoraAttention(int(q_tokens), int(k_tokens), int(heads), int(kv_heads), d, seqs, *st(q_strides, heads),
+                       *st(k_strides, kv_heads), *st(v_strides, kv_heads), *st(o_strides, heads), _act(dtype),
+                       _act(out_dtype or dtype), 1 if causal else 0, float(d ** -0.5 if scale is None else scale),
+                       _device_ints(q_offsets, "q_offsets", 1), _device_ints(k_offsets, "k_offsets", seqs + 1),
+                       _device_ints(k_lens, "k_lens", seqs))
+    at.vectors = (q_offsets, k_offsets, k_lens)
+    return at
+
+
+def lora_attention_workspace_bytes(at: LoraAttention, backward=False) -> int:
+    return int(lib().lora_attention_workspace_bytes(C.byref(at), 1 if backward else 0))
+
+
+def _attn_ptr(at, t, name, of, out):
+    """Device pointer of a tensor laid out like Q, K, V or O."""
+    n, h = (at.q_tokens, at.heads) if of in "qo" else (at.k_tokens, at.kv_heads)
+    return _strided(t, name, n, h, at.head_dim, getattr(at, "ld" + of), getattr(at, "h" + of),
+                    at.out_dtype if out else at.dtype)
+
+
+def lora_attention_forward(at: LoraAttention, Q, K, V, O, lse=None, ws=None, stream=None):
+    """O = attention of Q over K and V; lse [heads, q_tokens] float32 receives
+    what the backward needs.  `ws` is taken from torch's allocator when one is
+    needed and it is None."""
+    ptrs = [_attn_ptr(at, Q, "Q", "q", 0), _attn_ptr(at, K, "K", "k", 0), _attn_ptr(at, V, "V", "v", 0),
+            _attn_ptr(at, O, "O", "o", 1), _sized(lse, "lse", at.heads * at.q_tokens)]
+    if ws is None:
+        need = int(lib().lora_attention_workspace_bytes(C.byref(at), 0))
+        if need:
+            ws = _own_ws(need, O.device, stream)
+    rc = lib().lora_attention_forward(C.byref(at), *ptrs, _ptr(ws, "ws", None),
+                                      0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _check("lora_attention_forward", rc)
+
+
+def lora_attention_backward(at: LoraAttention, Q, K, V, O, dO, lse, dQ, dK, dV, ws=None, stream=None):
+    """Gradients of lora_attention_forward from dO; `ws` is taken from torch's
+    allocator when None."""
+    ptrs = [_attn_ptr(at, Q, "Q", "q", 0), _attn_ptr(at, K, "K", "k", 0), _attn_ptr(at, V, "V", "v", 0),
+            _attn_ptr(at, O, "O", "o", 1), _attn_ptr(at, dO, "dO", "o", 1),
+            _sized(lse, "lse", at.heads * at.q_tokens), _attn_ptr(at, dQ, "dQ", "q", 1),
+            _attn_ptr(at, dK, "dK", "k", 1), _attn_ptr(at, dV, "dV", "v", 1)]
+    if ws is None:
+        ws = _own_ws(max(16, int(lib().lora_attention_workspace_bytes(C.byref(at), 1))), dQ.device, stream)
+    rc = lib().lora_attention_backward(C.byref(at), *ptrs, _ptr(ws, "ws", None), ws.numel() * ws.element_size(),
+                                       _stream(stream))
+    _check("lora_attention_backward", rc)
 
 
 def lora_set_bf16_config(cfg: int):

@@ -505,6 +505,106 @@ int lora_norm_backward(const lora_norm* norm, const void* X, int n_dy, const voi
                        const float* stats, void* dX, float* dgamma, float* dbeta, int accumulate,
                        void* ws, size_t ws_bytes, void* stream);
 
+/* Heads: the norm and rotation of query and key heads, between a layer's
+ * projections and its attention.  For token t and head h, with D = head_dim
+ * and R = rot_dim:
+ *   z = x rstd gamma, rstd = 1 / sqrt(sum x^2 / D + eps)   (norm == 0: z = x)
+ *   (y_a, y_b) = (z_a cos - z_b sin, z_b cos + z_a sin), the angle being
+ *   positions[t] freqs[i], for the pairs i < R/2: (a, b) = (i, i + R/2), or
+ *   (2i, 2i + 1) with interleaved;  y = z past R
+ *   dx, dgamma (+)= the gradients (dgamma over all tokens and heads)
+ * Angles are reduced in float64, everything else is float32 with one rounding
+ * of Y or dX; dgamma is summed in float32 within a block and in double over
+ * the blocks, in a fixed order.  X and dX have x_dtype, Y and dY y_dtype;
+ * tokens are ldx and ldy elements apart, heads hx and hy (either order of the
+ * two in memory, no overlap).  Any head_dim up to 256 is accepted; head_dim and
+ * rot_dim multiples of 8, strides of 4 and rows aligned to 4 elements run
+ * faster.  With norm and rot_dim zero a call only converts (values, say). */
+typedef struct lora_heads {
+  int64_t tokens, heads, head_dim;
+  int64_t rot_dim;          /* even, <= head_dim; 0: no rotation           */
+  int64_t ldx, hx;          /* elements between tokens and heads of X, dX  */
+  int64_t ldy, hy;          /* of Y, dY                                    */
+  int32_t x_dtype, y_dtype; /* LORA_F32 or LORA_BF16                       */
+  int32_t norm;             /* 0: none, else RMS over the head             */
+  int32_t interleaved;
+  const float* gamma;       /* [head_dim] or NULL (ones; NULL without norm) */
+  const double* freqs;      /* [rot_dim / 2] radians a position, or NULL   */
+  float eps;                /* >= 0                                        */
+} lora_heads;
+
+/* One call takes n (1..LORA_MAX_GROUP) sets of heads of the same tokens
+ * (queries, keys, values).  positions: device int32 [tokens], NULL if nothing
+ * is rotated.  Y may be X itself where types and strides are equal. */
+int lora_heads_forward(int n, const lora_heads* heads, const void* const* X, void* const* Y,
+                       const int32_t* positions, void* stream);
+
+/* X is the forward's (not read without norm, then it may be NULL); dX and
+ * dgamma may be NULL as a whole or per set, not both; dgamma needs norm.
+ * accumulate != 0 adds into dgamma.  dX may be dY itself where types and
+ * strides are equal.  ws: lora_heads_workspace_bytes when a dgamma is wanted. */
+size_t lora_heads_workspace_bytes(int n, const lora_heads* heads);
+int lora_heads_backward(int n, const lora_heads* heads, const void* const* X, const void* const* dY,
+                        void* const* dX, float* const* dgamma, const int32_t* positions, int accumulate,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* Attention over packed sequences.  Sequence i's queries are rows q_offsets[i]
+ * .. q_offsets[i+1] - 1 of Q, its keys k_len rows of K and V from k_offsets[i],
+ * k_len = k_lens[i] if given, at most (and without k_lens)
+ * k_offsets[i+1] - k_offsets[i].  With lq and lk its lengths, query j sees keys
+ * 0 .. j + lk - lq (causal: queries are the last of the keys; lk > lq where
+ * keys reach back before them) or all lk.  Query head h reads key head
+ * h / (heads / kv_heads).  For each query and head:
+ *   s = scale q k^T over the keys it sees,  lse = log sum exp s,  p = exp(s - lse)
+ *   o = p v
+ * and, with do the gradient of o and delta = do . o:
+ *   ds = p (do v^T - delta),  dq = scale ds k,  dk = scale sum ds^T q,
+ *   dv = sum p^T do   (sums over the queries and heads that read the key)
+ * A query that sees no key gets o = 0, lse = -inf and dq = 0; a key that no
+ * query sees gets zero gradients.  Rows outside the sequences (and past a
+ * k_len) are neither read into any result nor written.  A non-finite value
+ * reaches results of its own sequence only, there also those of rows that do
+ * not see it.
+ *
+ * Q, K and V have type dtype; O, dO, dQ, dK and dV out_dtype (float32 with a
+ * float32 dtype).  Scores, softmax and all sums are float32; with bf16 the
+ * weights p and ds (and dO, if float32) are rounded to bf16 once, as operands
+ * of their products.  Offsets and lengths are device int32 and read by the
+ * kernels: offsets must not decrease, and the query rows and key rows of
+ * different sequences must not overlap; what points outside the buffers is
+ * cut to them.  Each tensor has ld elements between tokens and h between heads
+ * (either order of the two in memory, no overlap); gradients have the strides
+ * of what they are gradients of.  head_dim is a multiple of 8 up to 128, strides
+ * and pointers are 16-byte aligned (LORA_E_ALIGN); heads must be a multiple of
+ * kv_heads, q_tokens heads, k_tokens and seqs heads below 2^30, ldk and ldv at most 2^22
+ * (LORA_E_SHAPE).  Outputs must not overlap inputs. */
+typedef struct lora_attention {
+  int64_t q_tokens, k_tokens;   /* rows of Q and of K and V                */
+  int64_t heads, kv_heads, head_dim, seqs;
+  int64_t ldq, hq;              /* Q, dQ                                   */
+  int64_t ldk, hk;              /* K, dK                                   */
+  int64_t ldv, hv;              /* V, dV                                   */
+  int64_t ldo, ho;              /* O, dO                                   */
+  int32_t dtype, out_dtype;     /* LORA_F32 or LORA_BF16                   */
+  int32_t causal;
+  float scale;                  /* > 0                                     */
+  const int32_t* q_offsets;     /* [seqs + 1]                              */
+  const int32_t* k_offsets;     /* [seqs + 1]                              */
+  const int32_t* k_lens;        /* [seqs] or NULL                          */
+} lora_attention;
+
+size_t lora_attention_workspace_bytes(const lora_attention* at, int backward);
+
+/* lse: float [heads, q_tokens] (4-byte aligned) for the backward, or NULL.
+ * ws: lora_attention_workspace_bytes(at, 0), NULL where that is 0. */
+int lora_attention_forward(const lora_attention* at, const void* Q, const void* K, const void* V, void* O,
+                           float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* O and lse are the forward's.  ws: lora_attention_workspace_bytes(at, 1). */
+int lora_attention_backward(const lora_attention* at, const void* Q, const void* K, const void* V,
+                            const void* O, const void* dO, const float* lse, void* dQ, void* dK,
+                            void* dV, void* ws, size_t ws_bytes, void* stream);
+
 /* Diagnostics: launch timing.  lora_profile_begin opens a profile that can
  * hold max_launches launches (it creates that many HIP event pairs once and
  * keeps them); until lora_profile_end, each kernel launch of the library is
