@@ -83,12 +83,50 @@ double attn_bytes(const lora_attention* a, int n) {
   return a->head_dim * (a->q_tokens * a->heads * (e + n * oe) + a->k_tokens * a->kv_heads * (2 * e + (n > 1 ? 2 * oe : 0)));
 }
 
+// The forward's kernel: 128 rows a block, or 32 rows with the keys of a stage
+// dealt to its waves where a sequence has no more; and the blocks that share a
+// row tile's keys, so that few rows still fill the chip, with 256 keys each at
+// least (by the sequences' mean room: lengths are known to the kernels only).
+struct FwdPlan {
+  bool few;
+  int64_t tiles, splits;
+};
+FwdPlan fwd_plan(const lora_attention* a) {
+  const int64_t group = a->heads / a->kv_heads;
+  FwdPlan f;
+  f.few = a->q_tokens * group <= 32 * a->seqs;
+  f.tiles = tile_count(a->q_tokens, group, a->seqs, f.few ? 32 : 128);
+  f.splits = clampi(cdiv(4 * kCUs, f.tiles * a->kv_heads), 1, clampi(a->k_tokens / a->seqs / 256, 1, 64));
+  if (!f.few && f.tiles * a->kv_heads >= kCUs) f.splits = 1;
+  return f;
+}
+// Bytes of the splits' sums, and of their maxima and weights behind them.
+size_t part_bytes(const lora_attention* a, const FwdPlan& f, bool all) {
+  const int64_t dp = a->head_dim > 64 ? 128 : 64, n = f.splits * a->heads * a->q_tokens;
+  return f.splits > 1 ? (size_t)(n * (all ? dp + 2 : dp)) * sizeof(float) : 0;
+}
+
+template <typename T, typename OT, int DP, int RW, int CW, int KT>
+void forward_by(const lora_attention* a, const AttnArgs& p, hipStream_t st) {
+  const int64_t blocks = (int64_t)p.tiles * p.kv;
+  {
+    prof::Scope ps("attn_fwd", a->q_tokens, a->k_tokens, a->heads, 4.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 1));
+    launch_n(attn_fwd_kernel<T, OT, DP, RW, CW, KT>, dim3((unsigned)(blocks * p.splits)), 64 * RW * CW, st, ps, p);
+  }
+  if (p.splits > 1) {
+    prof::Scope ps("attn_join", a->q_tokens, a->heads, p.splits, 0.0, 4.0 * p.splits * a->heads * a->q_tokens * DP);
+    launch_n(attn_join_kernel<OT, DP, 32 * RW>, dim3((unsigned)blocks), 256u, st, ps, p);
+  }
+}
 template <typename T, typename OT, int DP>
-void forward(const lora_attention* a, AttnArgs p, hipStream_t st) {
-  constexpr int RW = 4, KT = sizeof(T) == 2 ? 2 : 1;
-  p.tiles = (int32_t)tile_count(a->q_tokens, p.group, a->seqs, 32 * RW);
-  prof::Scope ps("attn_fwd", a->q_tokens, a->k_tokens, a->heads, 4.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 1));
-  launch_n(attn_fwd_kernel<T, OT, DP, RW, KT>, dim3((unsigned)(p.tiles * p.kv)), 64 * RW, st, ps, p);
+void forward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
+  const FwdPlan f = fwd_plan(a);
+  p.tiles = (int32_t)f.tiles;
+  p.splits = (int32_t)f.splits;
+  p.part = (float*)ws;
+  p.ml = (float*)((char*)ws + part_bytes(a, f, false));
+  if (f.few) forward_by<T, OT, DP, 1, sizeof(T) == 2 ? 4 : 2, 1>(a, p, st);
+  else forward_by<T, OT, DP, 4, 1, sizeof(T) == 2 ? 2 : 1>(a, p, st);
 }
 
 template <typename T, typename OT, int DP>
@@ -121,7 +159,7 @@ extern "C" {
 
 size_t lora_attention_workspace_bytes(const lora_attention* at, int backward_) {
   if (check_attn(at) != LORA_OK) return 0;
-  return backward_ ? (size_t)rup(at->heads * at->q_tokens * 4, 16) : 0;
+  return backward_ ? (size_t)rup(at->heads * at->q_tokens * 4, 16) : part_bytes(at, fwd_plan(at), true);
 }
 
 int lora_attention_forward(const lora_attention* at, const void* Q, const void* K, const void* V, void* O, float* lse,
@@ -135,7 +173,7 @@ int lora_attention_forward(const lora_attention* at, const void* Q, const void* 
   AttnArgs p = attn_args(at);
   p.Q = Q, p.K = K, p.V = V, p.O = O, p.lse = lse;
   by_type(at, [&](auto t, auto o, auto d) {
-    forward<decltype(t), decltype(o), decltype(d)::value>(at, p, (hipStream_t)stream);
+    forward<decltype(t), decltype(o), decltype(d)::value>(at, p, ws, (hipStream_t)stream);
   });
   return hip_status();
 }

@@ -30,10 +30,11 @@ struct AttnArgs {
   void *dQ, *dK, *dV;           // OT
   float* lse;                   // [heads][q_tokens], forward: may be NULL
   float* delta;                 // [heads][q_tokens] (workspace of the backward)
+  float *part, *ml;             // splits: sums [splits][kv][q_tokens G][DP], maximum and weight [..][2]
   const int32_t *qo, *ko, *kl;  // offsets [seqs + 1] and lengths [seqs] or NULL
   int64_t ldq, hq, ldk, hk, ldv, hv, ldo, ho;
   int64_t q_tokens, k_tokens;
-  int32_t seqs, kv, group, dim, causal, tiles;
+  int32_t seqs, kv, group, dim, causal, tiles, splits;
   float scale, c;               // c = scale log2 e
 };
 
@@ -232,86 +233,332 @@ LORA_DEV void store_4(OT* g, float a, float b, float c, float d) {
   else *reinterpret_cast<u32x2*>(g) = u32x2{cvt_bf16x2(a, b), cvt_bf16x2(c, d)};
 }
 // acc^T [d][row] times f to the row at g.
-template <int DP, typename OT>
-LORA_DEV void store_row(OT* g, const f32x16 (&acc)[DP / 32], float f, int dim, int half) {
+template <int DP, typename OT, int CW = 1>
+LORA_DEV void store_row(OT* g, const f32x16 (&acc)[DP / 32], float f, int dim, int half, int cw = 0) {
 #pragma unroll
   for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int d = 32 * dt + 8 * q + 4 * half;
-      if (d < dim)
+      if (d < dim && dt % CW == cw)
         store_4(g + d, acc[dt][4 * q] * f, acc[dt][4 * q + 1] * f, acc[dt][4 * q + 2] * f, acc[dt][4 * q + 3] * f);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  A block's RW waves hold 32 rows each.
+// LDS tiles that arrive by direct-to-LDS loads.  A load of a wave writes 1 KB,
+// 16 bytes a lane in order, so the swizzle is in the address that each lane
+// reads from; rows and values outside (the resource ends at the last row, and a
+// lane past dim asks for what lies behind it) arrive as zeros.
 // ---------------------------------------------------------------------------
-template <typename T, typename OT, int DP, int RW, int KT>
-__global__ __launch_bounds__(64 * RW) void attn_fwd_kernel(AttnArgs p) {
-  constexpr int NT = 64 * RW, BM = 32 * RW, BN = 32 * KT, KS = DP / Frag<T>::FK, DT = DP / 32;
-  typedef typename Frag<T>::V V;
-  __shared__ __attribute__((aligned(16))) T Ks[BN * DP];
-  __shared__ __attribute__((aligned(16))) T Vs[BN * DP];
-  const int kvh = (int)(blockIdx.x % p.kv), t = p.tiles - 1 - (int)(blockIdx.x / p.kv);
-  const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
+typedef __attribute__((address_space(3))) char lds_char;
+constexpr uint32_t kNowhere = 0xfffffff0u;
+
+// Buffer resource of `bytes` from base (raw addresses, zeros past the end).
+LORA_DEV u32x4 attn_rsrc(const void* base, int64_t bytes) {
+  const uint64_t b = (uint64_t)base;
+  return u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, (uint32_t)(bytes > 0xffffff00ll ? 0xffffff00ll : bytes), 0x00020000u};
+}
+// 16 bytes a lane from r at `at` to 1 KB of LDS from dst (uniform).  In asm,
+// since the compiler holds every transpose read of LDS behind all such loads
+// that it knows of; the kernels wait for theirs themselves, before the barrier
+// ahead of a stage's use.  M0 is the compiler's and is put back.  (The waits: a
+// VALU-written scalar, then M0, before the load that reads them.)
+LORA_DEV void load_lds16(u32x4 r, lds_char* dst, uint32_t at) {
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 3\n\t"
+      "buffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"((uint32_t)(uintptr_t)dst), "v"(at), "s"(r)
+      : "memory");
+}
+
+template <typename T, int DP, int ROWS, int NW>
+struct Tile {
+  static constexpr int ROWB = DP * (int)sizeof(T), BYTES = ROWS * ROWB, CPR = ROWB / 16, PER = BYTES / 1024 / NW;
+  static_assert(BYTES % (1024 * NW) == 0, "");
+  // Row and 16-byte chunk of memory that lane `lane` of load q reads.
+  LORA_DEV static int row(int wave, int q, int lane) { return (64 * (wave * PER + q) + lane) / CPR; }
+  LORA_DEV static int chunk(int wave, int q, int lane) { return (64 * (wave * PER + q) + lane) % CPR ^ attn_swz<T, DP>(row(wave, q, lane)); }
+  LORA_DEV static void load(u32x4 r, lds_char* tile, int wave, const uint32_t (&at)[PER]) {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) load_lds16(r, tile + 1024 * (wave * PER + q), at[q]);
+  }
+};
+
+// Every load so far, those that the compiler counts included.
+LORA_DEV void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
+// The lane's part of the addresses of lds_rows and lds_cols, from row r0 of a tile.
+template <typename T, int DP>
+LORA_DEV uint32_t rows_at(int r0, int lane) {
+  const int row = r0 + (lane & 31);
+  return (uint32_t)(row * (DP * (int)sizeof(T)) + (((lane >> 5) ^ attn_swz<T, DP>(row)) << 4));
+}
+template <typename T, int DP>
+LORA_DEV uint32_t cols_at(int r0, int lane) {
+  if constexpr (sizeof(T) == 2) {
+    const int i = lane & 15, g = lane >> 4, row = r0 + 4 * (g >> 1) + (i >> 2), col = 16 * (g & 1) + 4 * (i & 3);
+    return (uint32_t)(row * (DP * 2) + (((col >> 3) ^ attn_swz<T, DP>(row)) << 4) + ((col & 4) << 1));
+  } else {
+    const int row = r0 + 4 * (lane >> 5);
+    return (uint32_t)(row * (DP * 4) + ((((lane & 31) >> 2) ^ attn_swz<T, DP>(row)) << 4) + ((lane & 3) << 2));
+  }
+}
+// acc += (rows from `at`) times the register operand f, both along DP.
+template <typename T, int DP>
+LORA_DEV f32x16 mma_rows(lds_char* tile, uint32_t at, const typename Frag<T>::V (&f)[DP / Frag<T>::FK]) {
+  typedef __attribute__((address_space(3))) const typename Frag<T>::V LV;
+  f32x16 acc = {};
+#pragma unroll
+  for (int s = 0; s < DP / Frag<T>::FK; ++s)
+    acc = Frag<T>::mma(*(LV*)(tile + (at ^ (uint32_t)(s << 5))), f[s], acc);
+  return acc;
+}
+// acc[dt] += (32 rows from `at`)^T x, x a product's result with the same rows
+// down its registers.  bf16: values 8 u .. 8 u + 7 of lane half h are rows
+// 16 u + 4 h + 0..3 and 16 u + 8 + 4 h + 0..3, the transpose reads' order.
+template <typename T, int DP>
+LORA_DEV void mma_cols(f32x16 (&acc)[DP / 32], lds_char* tile, uint32_t at, const f32x16& x) {
+  constexpr int ROWB = DP * (int)sizeof(T);
+  if constexpr (sizeof(T) == 2) {
+    typedef __attribute__((address_space(3))) attn_s4 LV;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      u32x4 b;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = cvt_bf16x2(x[8 * u + 2 * e], x[8 * u + 2 * e + 1]);
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt) {
+        const attn_s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LV*)(tile + 16 * u * ROWB + (at ^ (uint32_t)(dt << 6))));
+        const attn_s4 hi =
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((LV*)(tile + (16 * u + 8) * ROWB + (at ^ (uint32_t)(dt << 6) ^ 32u)));
+        const u32x2 a0 = __builtin_bit_cast(u32x2, lo), a1 = __builtin_bit_cast(u32x2, hi);
+        acc[dt] = mfma32x32x16_bf16(u32x4{a0[0], a0[1], a1[0], a1[1]}, b, acc[dt]);
+      }
+    }
+  } else {
+    typedef __attribute__((address_space(3))) const float LV;
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt)
+        acc[dt] = mfma32x32x2(*(LV*)(tile + (8 * (v >> 2) + (v & 3)) * ROWB +
+                                     (at ^ (uint32_t)(dt << 7) ^ (uint32_t)((((v >> 2) & 1) * 8 ^ (v & 3)) << 4))),
+                              x[v], acc[dt]);
+  }
+}
+
+// The block's sequence and row tile.
+struct RowTile {
+  AttnSeq s;
+  int m0, rows, kvh;   // first row, rows of the sequence, key head
+};
+LORA_DEV RowTile attn_row_tile(const AttnArgs& p, int b, int BM) {
+  RowTile r;
+  r.kvh = b % p.kv;
+  const int t = p.tiles - 1 - b / p.kv;
   const int i = attn_find(p.qo, p.seqs, p.q_tokens, p.group, BM, t);
-  const AttnSeq sq = attn_seq(p, i);
-  const int m0 = (t - attn_first(p.qo, p.q_tokens, p.group, BM, i)) * BM, rows = sq.lq * p.group;
+  r.s = attn_seq(p, i);
+  r.m0 = (t - attn_first(p.qo, p.q_tokens, p.group, BM, i)) * BM;
+  r.rows = r.s.lq * p.group;
+  r.m0 = __builtin_amdgcn_readfirstlane(r.m0);
+  r.rows = __builtin_amdgcn_readfirstlane(r.rows);
+  r.s.q0 = __builtin_amdgcn_readfirstlane(r.s.q0);
+  r.s.k0 = __builtin_amdgcn_readfirstlane(r.s.k0);
+  r.s.lk = __builtin_amdgcn_readfirstlane(r.s.lk);
+  r.s.lq = __builtin_amdgcn_readfirstlane(r.s.lq);
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// Forward.  A block has RW waves of 32 rows, times CW that share a stage's keys
+// (few rows: single tokens over a cache).  A stage is BN keys of K and V in
+// LDS; the next one loads while one is used.  p.splits blocks share a row
+// tile's stages where there are few tiles, and attn_join_kernel adds them up.
+//
+// The running maximum is only raised where it grew by more than 8 (in powers of
+// two): the weights then stay under 2^8 and nothing is lost, and most stages
+// rescale no sums.
+// ---------------------------------------------------------------------------
+template <typename T, typename OT, int DP, int RW, int CW, int KT>
+__global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 ? 2 : 1) void attn_fwd_kernel(AttnArgs p) {
+  constexpr int NW = RW * CW, BM = 32 * RW, BN = 32 * KT * CW, KS = DP / Frag<T>::FK, DT = DP / 32;
+  typedef typename Frag<T>::V V;
+  typedef Tile<T, DP, BN, NW> Ti;
+  constexpr int STAGE = 2 * Ti::BYTES;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  lds_char* const lds = (lds_char*)smem;
+  const int split = (int)(blockIdx.x / p.kv) % p.splits;
+  const RowTile rt = attn_row_tile(p, (int)(blockIdx.x / p.kv / p.splits) * p.kv + (int)(blockIdx.x % p.kv), BM);
+  const AttnSeq sq = rt.s;
+  const int m0 = rt.m0, rows = rt.rows, kvh = rt.kvh;
   if (m0 < 0 || m0 >= rows) return;
+  const int lane = threadIdx.x & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave % RW, cw = wave / RW;
   // This lane's row (lanes past the last one repeat it) and the keys it sees.
-  const int m = m0 + 32 * wave + (lane & 31), mc = min(m, rows - 1);
+  const int m = m0 + 32 * rw + (lane & 31), mc = min(m, rows - 1);
   const int tok = mc / p.group, head = kvh * p.group + mc % p.group;
   const int lim = attn_limit(p, sq, tok);
-  const int most = attn_limit(p, sq, (min(m0 + BM, rows) - 1) / p.group);        // of the block's rows
-  const int least = attn_limit(p, sq, min(m0 + 32 * wave, rows - 1) / p.group);  // of the wave's
+  const int most = attn_limit(p, sq, (min(m0 + BM, rows) - 1) / p.group);      // of the block's rows
+  const int least = attn_limit(p, sq, min(m0 + 32 * rw, rows - 1) / p.group);  // of the wave's
+  const int stages = (most + BN - 1) / BN, per = (stages + p.splits - 1) / p.splits;
+  const int st0 = split * per, st1 = min(stages, st0 + per);
   V qf[KS];
   load_frags<T, DP>(qf, (const T*)p.Q + (sq.q0 + tok) * p.ldq + head * p.hq, p.dim, half);
   f32x16 o[DT] = {};
-  float mx = -INFINITY, m2 = 0.0f, l = 0.0f;   // maximum, maximum times c (0: none yet), this half's sum
+  float m2 = -INFINITY, l = 0.0f;   // maximum times c, this half's sum
   const T* Kg = (const T*)p.K + sq.k0 * p.ldk + kvh * p.hk;
   const T* Vg = (const T*)p.V + sq.k0 * p.ldv + kvh * p.hv;
-  for (int kb = 0; kb < most; kb += BN) {
-    __syncthreads();
-    stage_rows<T, DP, BN, NT, T>(Ks, p.dim, [&](int r) { return kb + r < sq.lk ? Kg + (kb + r) * p.ldk : nullptr; });
-    stage_rows<T, DP, BN, NT, T>(Vs, p.dim, [&](int r) { return kb + r < sq.lk ? Vg + (kb + r) * p.ldv : nullptr; });
-    __syncthreads();
+  uint32_t ka[Ti::PER], va[Ti::PER];
+#pragma unroll
+  for (int q = 0; q < Ti::PER; ++q) {
+    const int r = Ti::row(wave, q, lane), d = Ti::chunk(wave, q, lane) * Frag<T>::E;
+    ka[q] = d < p.dim ? (uint32_t)((r * p.ldk + d) * (int)sizeof(T)) : kNowhere;
+    va[q] = d < p.dim ? (uint32_t)((r * p.ldv + d) * (int)sizeof(T)) : kNowhere;
+  }
+  // Stages load in order: the next one's first row, and bytes from there to the last row's end.
+  const int64_t kstep = BN * p.ldk * (int)sizeof(T), vstep = BN * p.ldv * (int)sizeof(T);
+  const char* kp = (const char*)Kg + st0 * kstep;
+  const char* vp = (const char*)Vg + st0 * vstep;
+  int64_t kleft = ((sq.lk - 1) * p.ldk + p.dim) * (int)sizeof(T) - st0 * kstep;
+  int64_t vleft = ((sq.lk - 1) * p.ldv + p.dim) * (int)sizeof(T) - st0 * vstep;
+  auto load = [&](int buf) {
+    Ti::load(attn_rsrc(kp, kleft), lds + buf * STAGE, wave, ka);
+    Ti::load(attn_rsrc(vp, vleft), lds + buf * STAGE + Ti::BYTES, wave, va);
+    kp += kstep, vp += vstep, kleft -= kstep, vleft -= vstep;
+  };
+  const uint32_t kat = rows_at<T, DP>(32 * KT * cw, lane), vat = cols_at<T, DP>(32 * KT * cw, lane);
+  auto step = [&](int st, auto B) {
+    constexpr int buf = decltype(B)::value;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (st + 1 < st1) load(buf ^ 1);
+    lds_char* const Ks = lds + buf * STAGE;
+    lds_char* const Vs = Ks + Ti::BYTES;
+    const int kb = st * BN + 32 * KT * cw;
     f32x16 s[KT];
-    float top = mx;
+    float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < KT; ++j) {
-      s[j] = mma_rows<T, DP>(Ks, 32 * j + (lane & 31), qf, half);
-      if (kb + BN > least) {
+    for (int j = 0; j < KT; ++j) s[j] = mma_rows<T, DP>(Ks + 32 * j * Ti::ROWB, kat, qf);
+    if (kb + 32 * KT > least) {
 #pragma unroll
-        for (int v = 0; v < 16; ++v)
-          if (kb + 32 * j + row32(v, lane) >= lim) s[j][v] = -INFINITY;
-      }
+      for (int j = 0; j < KT; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[j][v] = kb + 32 * j + row32(v, lane) >= lim ? -INFINITY : s[j][v];
+    }
+#pragma unroll
+    for (int j = 0; j < KT; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) top = fmaxf(top, s[j][v]);
-    }
-    top = fmaxf(top, other_half(top));
-    const float now = top == -INFINITY ? 0.0f : top * p.c;
-    const float old = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m2 - now);
-    mx = top;
-    m2 = now;
-    l *= old;
+    top = fmaxf(top, other_half(top)) * p.c;
+    // (not raised from -inf to -inf; a NaN never raises it and shows in the sum)
+    if (__any(top > m2 + 8.0f)) {
+      const float now = fmaxf(top, m2), old = m2 == now ? 1.0f : __builtin_amdgcn_exp2f(m2 - now);
+      m2 = now;
+      l *= old;
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) o[dt] *= old;
+      for (int dt = 0; dt < DT; ++dt) o[dt] *= old;
+    }
+    const float sub = m2 == -INFINITY ? 0.0f : m2;
 #pragma unroll
     for (int j = 0; j < KT; ++j) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        s[j][v] = __builtin_amdgcn_exp2f(fmaf(s[j][v], p.c, -now));
+        s[j][v] = __builtin_amdgcn_exp2f(fmaf(s[j][v], p.c, -sub));
         l += s[j][v];
       }
-      mma_cols<T, DP>(o, Vs, 32 * j, s[j], lane);
+      mma_cols<T, DP>(o, Vs + 32 * j * Ti::ROWB, vat, s[j]);
     }
+  };
+  if (st0 < st1) load(0);
+  wait_loads();   // Q too: a wait that the compiler placed in the loop would hold up the stages
+  for (int st = st0; st < st1; st += 2) {
+    step(st, std::integral_constant<int, 0>{});
+    if (st + 1 < st1) step(st + 1, std::integral_constant<int, 1>{});
   }
   l += other_half(l);
+  if constexpr (CW > 1) {
+    // Each wave takes some of the columns of all CW sums, in wave order.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    f32x4* sums = reinterpret_cast<f32x4*>(smem);             // [NW][DT][4][64]
+    f32x2* mls = reinterpret_cast<f32x2*>(sums + NW * DT * 256);   // [NW][64]
+    static_assert(NW * DT * 4096 + NW * 512 <= 2 * STAGE, "");
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sums[((wave * DT + dt) * 4 + q) * 64 + lane] = f32x4{o[dt][4 * q], o[dt][4 * q + 1], o[dt][4 * q + 2], o[dt][4 * q + 3]};
+    mls[wave * 64 + lane] = f32x2{m2, l};
+    __syncthreads();
+    float f[CW];
+    float all = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < CW; ++w) all = fmaxf(all, mls[(w * RW + rw) * 64 + lane][0]);
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < CW; ++w) {
+      const f32x2 x = mls[(w * RW + rw) * 64 + lane];
+      f[w] = x[0] == all ? 1.0f : __builtin_amdgcn_exp2f(x[0] - all);
+      l += f[w] * x[1];
+    }
+    m2 = all;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      if (dt % CW != cw) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4 x = {};
+#pragma unroll
+        for (int w = 0; w < CW; ++w) x += f[w] * sums[(((w * RW + rw) * DT + dt) * 4 + q) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[dt][4 * q + e] = x[e];
+      }
+    }
+  }
   if (m >= rows) return;
-  store_row<DP>((OT*)p.O + (sq.q0 + tok) * p.ldo + head * p.ho, o, l == 0.0f ? 0.0f : 1.0f / l, p.dim, half);
-  if (p.lse && half == 0)
+  if (p.splits > 1) {
+    const int64_t at = ((int64_t)split * p.kv + kvh) * (p.q_tokens * p.group) + (int64_t)sq.q0 * p.group + m;
+    store_row<DP, float, CW>(p.part + at * DP, o, 1.0f, DP, half, cw);
+    if (cw == 0 && half == 0) *reinterpret_cast<f32x2*>(p.ml + 2 * at) = f32x2{m2, l};
+    return;
+  }
+  store_row<DP, OT, CW>((OT*)p.O + (sq.q0 + tok) * p.ldo + head * p.ho, o, l == 0.0f ? 0.0f : 1.0f / l, p.dim, half, cw);
+  if (p.lse && cw == 0 && half == 0)
     p.lse[head * p.q_tokens + sq.q0 + tok] = l == 0.0f ? -INFINITY : (m2 + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// O and lse from the splits' sums, in split order: DP / 4 threads a row.
+template <typename OT, int DP, int BM>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
+  const RowTile rt = attn_row_tile(p, (int)blockIdx.x, BM);
+  if (rt.m0 < 0 || rt.m0 >= rt.rows) return;
+  const int d = 4 * (threadIdx.x % (DP / 4));
+  const int64_t R = p.q_tokens * p.group, step = R * p.kv;
+  for (int r = threadIdx.x / (DP / 4); r < BM && rt.m0 + r < rt.rows; r += 256 / (DP / 4)) {
+    const int m = rt.m0 + r, tok = m / p.group, head = rt.kvh * p.group + m % p.group;
+    const int64_t at = rt.kvh * R + (int64_t)rt.s.q0 * p.group + m;
+    float all = -INFINITY;
+#pragma unroll 8
+    for (int s = 0; s < p.splits; ++s) all = fmaxf(all, p.ml[2 * (at + s * step)]);
+    float l = 0.0f;
+    f32x4 o = {};
+#pragma unroll 8
+    for (int s = 0; s < p.splits; ++s) {
+      const f32x2 x = *reinterpret_cast<const f32x2*>(p.ml + 2 * (at + s * step));
+      const float f = x[0] == all ? 1.0f : __builtin_amdgcn_exp2f(x[0] - all);
+      l += f * x[1];
+      o += f * *reinterpret_cast<const f32x4*>(p.part + (at + s * step) * DP + d);
+    }
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;
+    if (d < p.dim)
+      store_4((OT*)p.O + (rt.s.q0 + tok) * p.ldo + head * p.ho + d, o[0] * f, o[1] * f, o[2] * f, o[3] * f);
+    if (p.lse && d == 0)
+      p.lse[head * p.q_tokens + rt.s.q0 + tok] = l == 0.0f ? -INFINITY : (all + __builtin_amdgcn_logf(l)) * kLn2;
+  }
 }
 
 // ---------------------------------------------------------------------------
