@@ -41,6 +41,9 @@ int check_attn(const lora_attention* a) {
       !apart(a->k_tokens, a->kv_heads, a->head_dim, a->ldv, a->hv) ||
       !apart(a->q_tokens, a->heads, a->head_dim, a->ldo, a->ho) || a->ldk > kMaxLd || a->ldv > kMaxLd)
     return LORA_E_SHAPE;
+  // Rows of a tile are addressed with 32-bit byte offsets from its first token.
+  const int64_t group = a->heads / a->kv_heads;
+  if (group * a->hq + 128 * a->ldq >= kMaxRows / 2 || group * a->ho + 128 * a->ldo >= kMaxRows / 2) return LORA_E_SHAPE;
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale) || !a->q_offsets || !a->k_offsets) return LORA_E_INVALID;
   const int64_t e = elem(a->dtype), oe = elem(a->out_dtype);
   if (a->head_dim % 8 || !al_to(a->ldq, e) || !al_to(a->hq, e) || !al_to(a->ldk, e) || !al_to(a->hk, e) ||
@@ -129,17 +132,59 @@ void forward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
   else forward_by<T, OT, DP, 4, 1, sizeof(T) == 2 ? 2 : 1>(a, p, st);
 }
 
+// The backward's pass over key tiles: 64 keys a block, and the blocks that share
+// a tile's rows.
+struct BwdPlan {
+  int64_t tiles, splits;
+};
+constexpr int64_t kBwdKeys = 64, kBwdRows = 64;
+BwdPlan bwd_plan(const lora_attention* a) {
+  const int64_t group = a->heads / a->kv_heads;
+  BwdPlan b;
+  b.tiles = tile_count(a->k_tokens, 1, a->seqs, kBwdKeys);
+  b.splits = clampi(cdiv(2 * kCUs, b.tiles * a->kv_heads), 1,
+                    clampi(a->q_tokens * group / a->seqs / (2 * kBwdRows), 1, 64));
+  return b;
+}
+// The backward's workspace: row statistics, dO rounded to bf16, split sums.
+struct BwdSpace {
+  size_t dO16, part, total;
+};
+BwdSpace bwd_space(const lora_attention* a) {
+  const int64_t dp = a->head_dim > 64 ? 128 : 64, rows = a->heads * a->q_tokens;
+  const BwdPlan b = bwd_plan(a);
+  BwdSpace w;
+  w.dO16 = (size_t)rup(2 * rows * 4, 256);
+  w.part = w.dO16 + (a->dtype != a->out_dtype ? (size_t)rup(rows * dp * 2, 256) : 0);
+  w.total = w.part + (b.splits > 1 ? (size_t)(b.splits * a->kv_heads * a->k_tokens * 2 * dp * 4) : 0);
+  return w;
+}
+
 template <typename T, typename OT, int DP>
-void backward(const lora_attention* a, AttnArgs p, hipStream_t st) {
-  constexpr int W = 4;
+void backward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
+  constexpr int W = 4, KT = sizeof(T) == 2 ? 2 : 1;
+  constexpr int QW = 2, QT = (int)kBwdRows / 32 / QW, KW = (int)kBwdKeys / 32;
+  const BwdSpace w = bwd_space(a);
+  p.stat = (float*)ws;
+  p.dO16 = (char*)ws + w.dO16;
+  p.part = (float*)((char*)ws + w.part);
   {
     p.tiles = (int32_t)tile_count(a->q_tokens, p.group, a->seqs, 32 * W);
     prof::Scope ps("attn_dq", a->q_tokens, a->k_tokens, a->heads, 6.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 3));
-    launch_n(attn_dq_kernel<T, OT, DP, W>, dim3((unsigned)(p.tiles * p.kv)), 64 * W, st, ps, p);
+    launch_n(attn_dq_kernel<T, OT, DP, W, KT>, dim3((unsigned)(p.tiles * p.kv)), 64 * W, st, ps, p);
   }
-  p.tiles = (int32_t)tile_count(a->k_tokens, 1, a->seqs, 32 * W);
-  prof::Scope ps("attn_dkv", a->q_tokens, a->k_tokens, a->heads, 8.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 2));
-  launch_n(attn_dkv_kernel<T, OT, DP, W>, dim3((unsigned)(p.tiles * p.kv)), 64 * W, st, ps, p);
+  const BwdPlan b = bwd_plan(a);
+  p.tiles = (int32_t)b.tiles;
+  p.splits = (int32_t)b.splits;
+  const int64_t blocks = b.tiles * p.kv;
+  {
+    prof::Scope ps("attn_dkv", a->q_tokens, a->k_tokens, a->heads, 8.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 2));
+    launch_n(attn_dkv_kernel<T, OT, DP, KW, QW, QT>, dim3((unsigned)(blocks * b.splits)), 64 * KW * QW, st, ps, p);
+  }
+  if (b.splits > 1) {
+    prof::Scope ps("attn_dkv_join", a->k_tokens, a->kv_heads, b.splits, 0.0, 8.0 * b.splits * a->kv_heads * a->k_tokens * DP);
+    launch_n(attn_dkv_join_kernel<OT, DP, (int)kBwdKeys>, dim3((unsigned)blocks), 256u, st, ps, p);
+  }
 }
 
 template <typename F>
@@ -159,7 +204,7 @@ extern "C" {
 
 size_t lora_attention_workspace_bytes(const lora_attention* at, int backward_) {
   if (check_attn(at) != LORA_OK) return 0;
-  return backward_ ? (size_t)rup(at->heads * at->q_tokens * 4, 16) : part_bytes(at, fwd_plan(at), true);
+  return backward_ ? bwd_space(at).total : part_bytes(at, fwd_plan(at), true);
 }
 
 int lora_attention_forward(const lora_attention* at, const void* Q, const void* K, const void* V, void* O, float* lse,
@@ -191,9 +236,9 @@ int lora_attention_backward(const lora_attention* at, const void* Q, const void*
   if (!ws || ws_bytes < need || !al16(ws)) return LORA_E_WORKSPACE;
   AttnArgs p = attn_args(at);
   p.Q = Q, p.K = K, p.V = V, p.O = const_cast<void*>(O), p.dO = dO, p.lse = const_cast<float*>(lse);
-  p.dQ = dQ, p.dK = dK, p.dV = dV, p.delta = (float*)ws;
+  p.dQ = dQ, p.dK = dK, p.dV = dV;
   by_type(at, [&](auto t, auto o, auto d) {
-    backward<decltype(t), decltype(o), decltype(d)::value>(at, p, (hipStream_t)stream);
+    backward<decltype(t), decltype(o), decltype(d)::value>(at, p, ws, (hipStream_t)stream);
   });
   return hip_status();
 }

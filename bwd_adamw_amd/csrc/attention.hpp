@@ -29,7 +29,8 @@ struct AttnArgs {
   const void* dO;               // OT
   void *dQ, *dK, *dV;           // OT
   float* lse;                   // [heads][q_tokens], forward: may be NULL
-  float* delta;                 // [heads][q_tokens] (workspace of the backward)
+  float* stat;                  // backward: [2][kv][q_tokens G] log-sums (powers of two) and delta
+  void* dO16;                   // backward, bf16 with float32 dO: dO rounded, [kv][q_tokens G][DP]
   float *part, *ml;             // splits: sums [splits][kv][q_tokens G][DP], maximum and weight [..][2]
   const int32_t *qo, *ko, *kl;  // offsets [seqs + 1] and lengths [seqs] or NULL
   int64_t ldq, hq, ldk, hk, ldv, hv, ldo, ho;
@@ -79,73 +80,7 @@ LORA_DEV int attn_swz(int row) {
   else return ((row & 2) << 1) ^ ((row >> 2) & 3);
 }
 
-// Operand with rows across lanes: row r0 + l % 32, fragment s of its values.
-template <typename T, int DP>
-LORA_DEV typename Frag<T>::V lds_rows(const T* tile, int row, int s, int half) {
-  constexpr int CPR = DP * (int)sizeof(T) / 16;
-  static_assert(CPR >= 8, "");
-  return *reinterpret_cast<const typename Frag<T>::V*>(
-      reinterpret_cast<const char*>(tile) + row * (DP * (int)sizeof(T)) + ((2 * s + half) ^ attn_swz<T, DP>(row)) * 16);
-}
-
 typedef short attn_s4 __attribute__((ext_vector_type(4)));
-// Operand with columns (d) across lanes and the contraction over rows, in the
-// order of a product's result: lane half h's values v = 8 u .. 8 u + 7 are rows
-// 16 u + 4 h + 0..3 and 16 u + 8 + 4 h + 0..3 of the 32 from r0.
-template <int DP>
-LORA_DEV u32x4 lds_cols(const uint16_t* tile, int r0, int u, int d0, int lane) {
-  const int i = lane & 15, g = lane >> 4;
-  const int row = r0 + 16 * u + 4 * (g >> 1) + (i >> 2);
-  const int col = d0 + 16 * (g & 1) + 4 * (i & 3);
-  auto at = [&](int r) {
-    return (__attribute__((address_space(3))) attn_s4*)(
-        (__attribute__((address_space(3))) const char*)tile + r * (DP * 2) +
-        (((col >> 3) ^ attn_swz<uint16_t, DP>(r)) << 4) + ((col & 4) << 1));
-  };
-  const attn_s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(row));
-  const attn_s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(row + 8));
-  const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
-  return u32x4{a[0], a[1], b[0], b[1]};
-}
-template <int DP>
-LORA_DEV float lds_cols(const float* tile, int r0, int v, int d0, int lane) {
-  const int row = r0 + row32(v, lane), col = d0 + (lane & 31);
-  return *reinterpret_cast<const float*>(reinterpret_cast<const char*>(tile) + row * (DP * 4) +
-                                         (((col >> 2) ^ attn_swz<float, DP>(row)) << 4) + ((col & 3) << 2));
-}
-
-// acc[dt] += tile[r0 .. r0 + 31][dt]^T x, x a product's result with the same 32
-// rows down its registers: the products over keys (forward, dQ) or rows (dK, dV).
-template <typename T, int DP>
-LORA_DEV void mma_cols(f32x16 (&acc)[DP / 32], const T* tile, int r0, const f32x16& x, int lane) {
-  if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      u32x4 b;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) b[e] = cvt_bf16x2(x[8 * u + 2 * e], x[8 * u + 2 * e + 1]);
-#pragma unroll
-      for (int dt = 0; dt < DP / 32; ++dt)
-        acc[dt] = mfma32x32x16_bf16(lds_cols<DP>(tile, r0, u, 32 * dt, lane), b, acc[dt]);
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < 16; ++v)
-#pragma unroll
-      for (int dt = 0; dt < DP / 32; ++dt)
-        acc[dt] = mfma32x32x2(lds_cols<DP>(tile, r0, v, 32 * dt, lane), x[v], acc[dt]);
-  }
-}
-
-// acc += rows of the tile times the register operand f (both along DP).
-template <typename T, int DP>
-LORA_DEV f32x16 mma_rows(const T* tile, int row, const typename Frag<T>::V (&f)[DP / Frag<T>::FK], int half) {
-  f32x16 acc = {};
-#pragma unroll
-  for (int s = 0; s < DP / Frag<T>::FK; ++s)
-    acc = Frag<T>::mma(lds_rows<T, DP>(tile, row, s, half), f[s], acc);
-  return acc;
-}
 
 // The other half's value of the same row.
 LORA_DEV float other_half(float x) {
@@ -211,21 +146,6 @@ LORA_DEV void load_frags(typename Frag<T>::V (&f)[DP / Frag<T>::FK], const OT* r
   }
 }
 
-// Rows of memory into an LDS tile [ROWS][DP]; `at(r)` gives row r's address or
-// NULL (zeros).  Values past dim are zero.
-template <typename T, int DP, int ROWS, int NT, typename OT, typename F>
-LORA_DEV void stage_rows(T* tile, int dim, F at) {
-  constexpr int CPR = DP * (int)sizeof(T) / 16, E = Frag<T>::E;
-#pragma unroll
-  for (int c = threadIdx.x; c < ROWS * CPR; c += NT) {
-    const int row = c / CPR, ch = c % CPR;
-    const OT* g = at(row);
-    const typename Frag<T>::V v = g && ch * E < dim ? frag_of<T>(g + ch * E) : typename Frag<T>::V{};
-    *reinterpret_cast<typename Frag<T>::V*>(reinterpret_cast<char*>(tile) + row * (DP * (int)sizeof(T)) +
-                                            (ch ^ attn_swz<T, DP>(row)) * 16) = v;
-  }
-}
-
 // Four neighbouring results of one row.
 template <typename OT>
 LORA_DEV void store_4(OT* g, float a, float b, float c, float d) {
@@ -273,7 +193,21 @@ LORA_DEV void load_lds16(u32x4 r, lds_char* dst, uint32_t at) {
       "buffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(m0)
-      : "s"((uint32_t)(uintptr_t)dst), "v"(at), "s"(r)
+      : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)dst)), "v"(at), "s"(r)
+      : "memory");
+}
+
+// The same for 4 bytes a lane, 256 in all.
+LORA_DEV void load_lds4(u32x4 r, lds_char* dst, uint32_t at) {
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 3\n\t"
+      "buffer_load_dword %2, %3, 0 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)dst)), "v"(at), "s"(r)
       : "memory");
 }
 
@@ -386,7 +320,7 @@ LORA_DEV RowTile attn_row_tile(const AttnArgs& p, int b, int BM) {
 // rescale no sums.
 // ---------------------------------------------------------------------------
 template <typename T, typename OT, int DP, int RW, int CW, int KT>
-__global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 ? 2 : 1) void attn_fwd_kernel(AttnArgs p) {
+__global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 && CW == 1 ? 2 : 1) void attn_fwd_kernel(AttnArgs p) {
   constexpr int NW = RW * CW, BM = 32 * RW, BN = 32 * KT * CW, KS = DP / Frag<T>::FK, DT = DP / 32;
   typedef typename Frag<T>::V V;
   typedef Tile<T, DP, BN, NW> Ti;
@@ -570,18 +504,20 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
 // dV).  S and dP are computed in both: 7 products where one pass would take 5,
 // but dQ would then be summed over key tiles in memory, in no fixed order.
 // ---------------------------------------------------------------------------
-template <typename T, typename OT, int DP, int RW>
-__global__ __launch_bounds__(64 * RW) void attn_dq_kernel(AttnArgs p) {
-  constexpr int NT = 64 * RW, BM = 32 * RW, BN = 32, KS = DP / Frag<T>::FK, DT = DP / 32;
+template <typename T, typename OT, int DP, int RW, int KT>
+__global__ __launch_bounds__(64 * RW, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(AttnArgs p) {
+  constexpr int BM = 32 * RW, BN = 32 * KT, KS = DP / Frag<T>::FK, DT = DP / 32;
+  constexpr bool MIXED = !std::is_same_v<T, OT>;
   typedef typename Frag<T>::V V;
-  __shared__ __attribute__((aligned(16))) T Ks[BN * DP];
-  __shared__ __attribute__((aligned(16))) T Vs[BN * DP];
-  const int kvh = (int)(blockIdx.x % p.kv), t = p.tiles - 1 - (int)(blockIdx.x / p.kv);
-  const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
-  const int i = attn_find(p.qo, p.seqs, p.q_tokens, p.group, BM, t);
-  const AttnSeq sq = attn_seq(p, i);
-  const int m0 = (t - attn_first(p.qo, p.q_tokens, p.group, BM, i)) * BM, rows = sq.lq * p.group;
+  typedef Tile<T, DP, BN, RW> Ti;
+  constexpr int STAGE = 2 * Ti::BYTES;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  lds_char* const lds = (lds_char*)smem;
+  const RowTile rt = attn_row_tile(p, (int)blockIdx.x, BM);
+  const AttnSeq sq = rt.s;
+  const int m0 = rt.m0, rows = rt.rows, kvh = rt.kvh;
   if (m0 < 0 || m0 >= rows) return;
+  const int lane = threadIdx.x & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = m0 + 32 * wave + (lane & 31), mc = min(m, rows - 1);
   const int tok = mc / p.group, head = kvh * p.group + mc % p.group;
   const int lim = attn_limit(p, sq, tok);
@@ -593,105 +529,261 @@ __global__ __launch_bounds__(64 * RW) void attn_dq_kernel(AttnArgs p) {
   const OT* orow = (const OT*)p.O + (sq.q0 + tok) * p.ldo + head * p.ho;
   load_frags<T, DP>(df, dor, p.dim, half);
   float delta = 0.0f;
-  for (int d = 4 * half; d < p.dim; d += 8) {
-    f32x4 a, b;
-    if constexpr (sizeof(OT) == 4) {
-      a = *reinterpret_cast<const f32x4*>(dor + d);
-      b = *reinterpret_cast<const f32x4*>(orow + d);
-    } else {
-      const u32x2 x = *reinterpret_cast<const u32x2*>(dor + d), y = *reinterpret_cast<const u32x2*>(orow + d);
-      a = f32x4{__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
-                __uint_as_float(x[1] & 0xffff0000u)};
-      b = f32x4{__uint_as_float(y[0] << 16), __uint_as_float(y[0] & 0xffff0000u), __uint_as_float(y[1] << 16),
-                __uint_as_float(y[1] & 0xffff0000u)};
-    }
+#pragma unroll
+  for (int k = 0; k < DP / 8; ++k) {
+    const int d = 8 * k + 4 * half;
+    if (d >= p.dim) continue;
+    const f32x4 a = load4(dor + d), b = load4(orow + d);
     delta += (a[0] * b[0] + a[1] * b[1]) + (a[2] * b[2] + a[3] * b[3]);
   }
   delta += other_half(delta);
-  const int64_t at = head * p.q_tokens + sq.q0 + tok;
-  if (half == 0 && m < rows) p.delta[at] = delta;
-  const float lse2 = p.lse[at] * kLog2e;
+  const float lse = p.lse[head * p.q_tokens + sq.q0 + tok];
+  const float lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;   // (no keys: nothing below counts)
+  const int64_t R = p.q_tokens * p.group, at = kvh * R + (int64_t)sq.q0 * p.group + m;
+  if (m < rows) {   // for the pass over key tiles
+    if (half == 0) {
+      p.stat[at] = lse2;
+      p.stat[p.kv * R + at] = delta;
+    }
+    if constexpr (MIXED) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        *reinterpret_cast<V*>((T*)p.dO16 + at * DP + Frag<T>::FK * s + Frag<T>::E * half) = df[s];
+    }
+  }
   f32x16 dq[DT] = {};
   const T* Kg = (const T*)p.K + sq.k0 * p.ldk + kvh * p.hk;
   const T* Vg = (const T*)p.V + sq.k0 * p.ldv + kvh * p.hv;
-  for (int kb = 0; kb < most; kb += BN) {
-    __syncthreads();
-    stage_rows<T, DP, BN, NT, T>(Ks, p.dim, [&](int r) { return kb + r < sq.lk ? Kg + (kb + r) * p.ldk : nullptr; });
-    stage_rows<T, DP, BN, NT, T>(Vs, p.dim, [&](int r) { return kb + r < sq.lk ? Vg + (kb + r) * p.ldv : nullptr; });
-    __syncthreads();
-    f32x16 s = mma_rows<T, DP>(Ks, lane & 31, qf, half);
-    const f32x16 dp = mma_rows<T, DP>(Vs, lane & 31, df, half);
+  uint32_t ka[Ti::PER], va[Ti::PER];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], p.c, -lse2)) * (dp[v] - delta);
-    if (kb + BN > least) {   // after the products: what a masked score gives must not count
+  for (int q = 0; q < Ti::PER; ++q) {
+    const int r = Ti::row(wave, q, lane), d = Ti::chunk(wave, q, lane) * Frag<T>::E;
+    ka[q] = d < p.dim ? (uint32_t)((r * p.ldk + d) * (int)sizeof(T)) : kNowhere;
+    va[q] = d < p.dim ? (uint32_t)((r * p.ldv + d) * (int)sizeof(T)) : kNowhere;
+  }
+  const int64_t kstep = BN * p.ldk * (int)sizeof(T), vstep = BN * p.ldv * (int)sizeof(T);
+  const char* kp = (const char*)Kg;
+  const char* vp = (const char*)Vg;
+  int64_t kleft = ((sq.lk - 1) * p.ldk + p.dim) * (int)sizeof(T), vleft = ((sq.lk - 1) * p.ldv + p.dim) * (int)sizeof(T);
+  auto load = [&](int buf) {
+    Ti::load(attn_rsrc(kp, kleft), lds + buf * STAGE, wave, ka);
+    Ti::load(attn_rsrc(vp, vleft), lds + buf * STAGE + Ti::BYTES, wave, va);
+    kp += kstep, vp += vstep, kleft -= kstep, vleft -= vstep;
+  };
+  const uint32_t rat = rows_at<T, DP>(0, lane), cat = cols_at<T, DP>(0, lane);
+  auto step = [&](int kb, auto B) {
+    constexpr int buf = decltype(B)::value;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kb + BN < most) load(buf ^ 1);
+    lds_char* const Ks = lds + buf * STAGE;
+    lds_char* const Vs = Ks + Ti::BYTES;
 #pragma unroll
-      for (int v = 0; v < 16; ++v)
-        if (kb + row32(v, lane) >= lim) s[v] = 0.0f;
+    for (int j = 0; j < KT; ++j) {
+      f32x16 s = mma_rows<T, DP>(Ks + 32 * j * Ti::ROWB, rat, qf);
+      const f32x16 dp = mma_rows<T, DP>(Vs + 32 * j * Ti::ROWB, rat, df);
+#pragma unroll
+      for (int v = 0; v < 16; ++v) s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], p.c, -lse2)) * (dp[v] - delta);
+      if (kb + 32 * j + 32 > least) {   // after the products: what a masked score gives must not count
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[v] = kb + 32 * j + row32(v, lane) >= lim ? 0.0f : s[v];
+      }
+      mma_cols<T, DP>(dq, Ks + 32 * j * Ti::ROWB, cat, s);
     }
-    mma_cols<T, DP>(dq, Ks, 0, s, lane);
+  };
+  if (most > 0) load(0);
+  wait_loads();
+  for (int kb = 0; kb < most; kb += 2 * BN) {
+    step(kb, std::integral_constant<int, 0>{});
+    if (kb + BN < most) step(kb + BN, std::integral_constant<int, 1>{});
   }
   if (m >= rows) return;
   store_row<DP>((OT*)p.dQ + (sq.q0 + tok) * p.ldq + head * p.hq, dq, p.scale, p.dim, half);
 }
 
-// dK and dV of 32 keys a wave, over all rows that see them.
-template <typename T, typename OT, int DP, int KW>
-__global__ __launch_bounds__(64 * KW) void attn_dkv_kernel(AttnArgs p) {
-  constexpr int NT = 64 * KW, BK = 32 * KW, BQ = 32, KS = DP / Frag<T>::FK, DT = DP / 32;
+// The block's sequence and key tile.
+struct KeyTile {
+  AttnSeq s;
+  int k0, kvh;
+};
+LORA_DEV KeyTile attn_key_tile(const AttnArgs& p, int b, int BK) {
+  KeyTile r;
+  r.kvh = b % p.kv;
+  const int t = b / p.kv, i = attn_find(p.ko, p.seqs, p.k_tokens, 1, BK, t);
+  r.s = attn_seq(p, i);
+  r.k0 = __builtin_amdgcn_readfirstlane((t - attn_first(p.ko, p.k_tokens, 1, BK, i)) * BK);
+  r.s.q0 = __builtin_amdgcn_readfirstlane(r.s.q0);
+  r.s.k0 = __builtin_amdgcn_readfirstlane(r.s.k0);
+  r.s.lk = __builtin_amdgcn_readfirstlane(r.s.lk);
+  r.s.lq = __builtin_amdgcn_readfirstlane(r.s.lq);
+  return r;
+}
+
+// dK and dV.  A block's KW waves hold 32 keys each in registers, times QW that
+// share a stage's rows; a stage is BQ rows of Q and dO (gathered: G heads of
+// neighbouring tokens) with their log-sums and deltas.  p.splits blocks share a
+// key tile's stages where there are few tiles.
+template <typename T, typename OT, int DP, int KW, int QW, int QT>
+__global__ __launch_bounds__(64 * KW * QW, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(AttnArgs p) {
+  constexpr int NW = KW * QW, BK = 32 * KW, BQ = 32 * QW * QT, KS = DP / Frag<T>::FK, DT = DP / 32;
+  constexpr bool MIXED = !std::is_same_v<T, OT>;
   typedef typename Frag<T>::V V;
-  __shared__ __attribute__((aligned(16))) T Qs[BQ * DP];
-  __shared__ __attribute__((aligned(16))) T Ds[BQ * DP];
-  __shared__ __attribute__((aligned(16))) float ls[BQ], des[BQ];
-  __shared__ int lims[BQ];
-  const int kvh = (int)(blockIdx.x % p.kv), t = (int)(blockIdx.x / p.kv);
-  const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
-  const int i = attn_find(p.ko, p.seqs, p.k_tokens, 1, BK, t);
-  const AttnSeq sq = attn_seq(p, i);
-  const int k0 = (t - attn_first(p.ko, p.k_tokens, 1, BK, i)) * BK, rows = sq.lq * p.group;
+  typedef Tile<T, DP, BQ, NW> Ti;
+  constexpr int SB = BQ < 64 ? 256 : 4 * BQ, STAGE = 2 * Ti::BYTES + 2 * SB;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  lds_char* const lds = (lds_char*)smem;
+  const int split = (int)(blockIdx.x / p.kv) % p.splits;
+  const KeyTile kt = attn_key_tile(p, (int)(blockIdx.x / p.kv / p.splits) * p.kv + (int)(blockIdx.x % p.kv), BK);
+  const AttnSeq sq = kt.s;
+  const int k0 = kt.k0, kvh = kt.kvh, rows = sq.lq * p.group;
   if (k0 < 0 || k0 >= sq.lk) return;
-  const int key = k0 + 32 * wave + (lane & 31), kc = min(key, sq.lk - 1);
+  const int lane = threadIdx.x & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = wave % KW, qw = wave / KW;
+  const int key = k0 + 32 * kw + (lane & 31), kc = min(key, sq.lk - 1);
   V kf[KS], vf[KS];
   load_frags<T, DP>(kf, (const T*)p.K + (sq.k0 + kc) * p.ldk + kvh * p.hk, p.dim, half);
   load_frags<T, DP>(vf, (const T*)p.V + (sq.k0 + kc) * p.ldv + kvh * p.hv, p.dim, half);
   f32x16 dk[DT] = {}, dv[DT] = {};
-  // The first row that sees one of the block's keys.
-  const int first = p.causal ? max(k0 - (sq.lk - sq.lq), 0) * p.group : 0;
-  for (int mb = first / BQ * BQ; mb < rows; mb += BQ) {
-    __syncthreads();
-    auto row = [&](int r, int64_t ld, int64_t h) {
-      const int m = mb + r;
-      return (sq.q0 + m / p.group) * ld + (kvh * p.group + m % p.group) * h;
-    };
-    stage_rows<T, DP, BQ, NT, T>(Qs, p.dim, [&](int r) {
-      return mb + r < rows ? (const T*)p.Q + row(r, p.ldq, p.hq) : nullptr;
-    });
-    stage_rows<T, DP, BQ, NT, OT>(Ds, p.dim, [&](int r) {
-      return mb + r < rows ? (const OT*)p.dO + row(r, p.ldo, p.ho) : nullptr;
-    });
-    if (threadIdx.x < BQ) {
-      const int m = mb + threadIdx.x;
-      const bool in = m < rows;
-      const int64_t at = in ? row(threadIdx.x, 1, p.q_tokens) : 0;
-      ls[threadIdx.x] = in ? p.lse[at] * kLog2e : 0.0f;
-      des[threadIdx.x] = in ? p.delta[at] : 0.0f;
-      lims[threadIdx.x] = in ? attn_limit(p, sq, m / p.group) : 0;
-    }
-    __syncthreads();
-    f32x16 s = mma_rows<T, DP>(Qs, lane & 31, kf, half);
-    f32x16 ds = mma_rows<T, DP>(Ds, lane & 31, vf, half);
+  // The first row that sees key j is sees(j): causal row m sees up to m / G + lk - lq.
+  auto sees = [&](int j) { return p.causal ? max(j - (sq.lk - sq.lq), 0) * p.group : 0; };
+  const int mine = sees(kc);
+  const int all = sees(min(k0 + 32 * kw + 31, sq.lk - 1));   // from here on rows see all of the wave's keys
+  const int some = sees(min(k0 + 32 * kw, sq.lk - 1));       // up to here, none
+  const int begin = sees(k0) / BQ, end = (rows + BQ - 1) / BQ, per = (max(end - begin, 0) + p.splits - 1) / p.splits;
+  const int st0 = begin + split * per, st1 = min(end, st0 + per);
+  const int64_t R = p.q_tokens * p.group, srow = kvh * R + (int64_t)sq.q0 * p.group;
+  const char* const Qg = (const char*)((const T*)p.Q + sq.q0 * p.ldq + kvh * p.group * p.hq);
+  const char* const Dg = MIXED ? (const char*)((const T*)p.dO16 + srow * DP)
+                               : (const char*)((const T*)p.dO + sq.q0 * p.ldo + kvh * p.group * p.ho);
+  // Row m0 + r of Q and dO relative to the token of row m0.
+  uint32_t qa[Ti::PER], da[Ti::PER];
+  auto addresses = [&](int first) {
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int r = row32(v, lane);
-      const bool in = key < lims[r];
-      s[v] = in ? __builtin_amdgcn_exp2f(fmaf(s[v], p.c, -ls[r])) : 0.0f;
-      ds[v] = in ? s[v] * (ds[v] - des[r]) : 0.0f;
+    for (int q = 0; q < Ti::PER; ++q) {
+      const int r = Ti::row(wave, q, lane), x = first + r, d = Ti::chunk(wave, q, lane) * Frag<T>::E;
+      const int64_t t = x / p.group, h = x % p.group;
+      qa[q] = d < p.dim ? (uint32_t)((t * p.ldq + h * p.hq + d) * (int)sizeof(T)) : kNowhere;
+      da[q] = MIXED ? (uint32_t)((r * DP + d) * (int)sizeof(T))
+                    : d < p.dim ? (uint32_t)((t * p.ldo + h * p.ho + d) * (int)sizeof(T)) : kNowhere;
     }
-    mma_cols<T, DP>(dv, Ds, 0, s, lane);
-    mma_cols<T, DP>(dk, Qs, 0, ds, lane);
+  };
+  const bool whole = BQ % p.group == 0;   // every stage starts at a token's first head
+  if (whole) addresses(0);
+  auto load = [&](int st, int buf) {
+    const int mb = st * BQ, t0 = mb / p.group;
+    if (!whole) addresses(mb - t0 * p.group);
+    const u32x4 rq = attn_rsrc(Qg + t0 * p.ldq * (int)sizeof(T), 1ll << 32);
+    const u32x4 rd = attn_rsrc(MIXED ? Dg + (int64_t)mb * DP * (int)sizeof(T) : Dg + t0 * p.ldo * (int)sizeof(T), 1ll << 32);
+    lds_char* const b = lds + buf * STAGE;
+    const int left = rows - mb;
+#pragma unroll
+    for (int q = 0; q < Ti::PER; ++q)
+      load_lds16(rq, b + 1024 * (wave * Ti::PER + q), Ti::row(wave, q, lane) < left ? qa[q] : kNowhere);
+#pragma unroll
+    for (int q = 0; q < Ti::PER; ++q)
+      load_lds16(rd, b + Ti::BYTES + 1024 * (wave * Ti::PER + q), Ti::row(wave, q, lane) < left ? da[q] : kNowhere);
+    // Past the last row: zeros, with which a row of zeros adds nothing.
+    static_assert(2 * (SB / 256) <= NW, "");
+    if (wave < 2 * (SB / 256)) {
+      const int which = wave / (SB / 256), part = wave % (SB / 256);
+      load_lds4(attn_rsrc(p.stat + which * p.kv * R + srow + mb, 4ll * left), b + 2 * Ti::BYTES + 256 * wave,
+                (uint32_t)(256 * part + 4 * lane));
+    }
+  };
+  const uint32_t rat = rows_at<T, DP>(32 * QT * qw, lane), cat = cols_at<T, DP>(32 * QT * qw, lane);
+  auto step = [&](int st, auto B) {
+    constexpr int buf = decltype(B)::value;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (st + 1 < st1) load(st + 1, buf ^ 1);
+    lds_char* const Qs = lds + buf * STAGE;
+    lds_char* const Ds = Qs + Ti::BYTES;
+    typedef __attribute__((address_space(3))) const f32x4 LV;
+#pragma unroll
+    for (int j = 0; j < QT; ++j) {
+      const int r0 = 32 * (QT * qw + j), mb = st * BQ + r0;
+      if (mb + 31 < some) continue;
+      lds_char* const stat = Ds + Ti::BYTES + 4 * (r0 + 4 * half);
+      f32x16 s = mma_rows<T, DP>(Qs + 32 * j * Ti::ROWB, rat, kf);
+      f32x16 ds = mma_rows<T, DP>(Ds + 32 * j * Ti::ROWB, rat, vf);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 ls = *(LV*)(stat + 32 * q), de = *(LV*)(stat + SB + 32 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = 4 * q + e;
+          s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], p.c, -ls[e]));
+          ds[v] = s[v] * (ds[v] - de[e]);
+        }
+      }
+      if (mb < all) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const bool in = mb + row32(v, lane) >= mine;
+          s[v] = in ? s[v] : 0.0f;
+          ds[v] = in ? ds[v] : 0.0f;
+        }
+      }
+      mma_cols<T, DP>(dv, Ds + 32 * j * Ti::ROWB, cat, s);
+      mma_cols<T, DP>(dk, Qs + 32 * j * Ti::ROWB, cat, ds);
+    }
+  };
+  if (st0 < st1) load(st0, 0);
+  wait_loads();
+  for (int st = st0; st < st1; st += 2) {
+    step(st, std::integral_constant<int, 0>{});
+    if (st + 1 < st1) step(st + 1, std::integral_constant<int, 1>{});
+  }
+  if constexpr (QW > 1) {   // added up in wave order, dK then dV
+    static_assert(KW * DT * 4096 <= 2 * STAGE, "");
+    f32x4* sums = reinterpret_cast<f32x4*>(smem) + kw * DT * 256 + lane;
+#pragma unroll
+    for (int w = 1; w < QW; ++w)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        f32x16(&acc)[DT] = k == 0 ? dk : dv;
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (qw == w) {
+#pragma unroll
+          for (int x = 0; x < 4 * DT; ++x)
+            sums[64 * x] = f32x4{acc[x >> 2][4 * (x & 3)], acc[x >> 2][4 * (x & 3) + 1], acc[x >> 2][4 * (x & 3) + 2],
+                                 acc[x >> 2][4 * (x & 3) + 3]};
+        }
+        __syncthreads();
+        if (qw == 0) {
+#pragma unroll
+          for (int x = 0; x < 4 * DT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[x >> 2][4 * (x & 3) + e] += sums[64 * x][e];
+        }
+      }
+    if (qw > 0) return;
   }
   if (key >= sq.lk) return;
+  if (p.splits > 1) {
+    float* g = p.part + (((int64_t)split * p.kv + kvh) * p.k_tokens + sq.k0 + key) * 2 * DP;
+    store_row<DP>(g, dk, 1.0f, DP, half);
+    store_row<DP>(g + DP, dv, 1.0f, DP, half);
+    return;
+  }
   store_row<DP>((OT*)p.dK + (sq.k0 + key) * p.ldk + kvh * p.hk, dk, p.scale, p.dim, half);
   store_row<DP>((OT*)p.dV + (sq.k0 + key) * p.ldv + kvh * p.hv, dv, 1.0f, p.dim, half);
+}
+
+// dK and dV from the splits' sums, in split order: DP / 2 threads a key.
+template <typename OT, int DP, int BK>
+__global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs p) {
+  const KeyTile kt = attn_key_tile(p, (int)blockIdx.x, BK);
+  if (kt.k0 < 0 || kt.k0 >= kt.s.lk) return;
+  const int x = 4 * (threadIdx.x % (DP / 2)), d = x % DP;
+  const int64_t step = p.k_tokens * p.kv * 2 * DP;
+  for (int r = threadIdx.x / (DP / 2); r < BK && kt.k0 + r < kt.s.lk; r += 256 / (DP / 2)) {
+    const int64_t key = kt.s.k0 + kt.k0 + r;
+    const f32x4 o = sum_parts4(p.part, step, p.splits, (kt.kvh * p.k_tokens + key) * 2 * DP + x);
+    if (d >= p.dim) continue;
+    if (x < DP)
+      store_4((OT*)p.dK + key * p.ldk + kt.kvh * p.hk + d, o[0] * p.scale, o[1] * p.scale, o[2] * p.scale, o[3] * p.scale);
+    else
+      store_4((OT*)p.dV + key * p.ldv + kt.kvh * p.hv + d, o[0], o[1], o[2], o[3]);
+  }
 }
 
 }  // namespace lora
