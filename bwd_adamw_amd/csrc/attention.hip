@@ -91,16 +91,18 @@ double attn_bytes(const lora_attention* a, int n) {
 // row tile's keys, so that few rows still fill the chip, with 256 keys each at
 // least (by the sequences' mean room: lengths are known to the kernels only).
 struct FwdPlan {
-  bool few;
+  int rw;                  // waves of 32 rows: 1 or 2 (times waves that share a stage's keys) or 4
   int64_t tiles, splits;
 };
 FwdPlan fwd_plan(const lora_attention* a) {
   const int64_t group = a->heads / a->kv_heads;
   FwdPlan f;
-  f.few = a->q_tokens * group <= 32 * a->seqs;
-  f.tiles = tile_count(a->q_tokens, group, a->seqs, f.few ? 32 : 128);
+  f.rw = a->q_tokens * group <= 32 * a->seqs                                     ? 1
+         : tile_count(a->q_tokens, group, a->seqs, 128) * a->kv_heads < kCUs ? 2
+                                                                             : 4;
+  f.tiles = tile_count(a->q_tokens, group, a->seqs, 32 * f.rw);
   f.splits = clampi(cdiv(4 * kCUs, f.tiles * a->kv_heads), 1, clampi(a->k_tokens / a->seqs / 256, 1, 64));
-  if (!f.few && f.tiles * a->kv_heads >= kCUs) f.splits = 1;
+  if (f.rw > 1 && f.tiles * a->kv_heads >= kCUs) f.splits = 1;
   return f;
 }
 // Bytes of the splits' sums, and of their maxima and weights behind them.
@@ -128,22 +130,29 @@ void forward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
   p.splits = (int32_t)f.splits;
   p.part = (float*)ws;
   p.ml = (float*)((char*)ws + part_bytes(a, f, false));
-  if (f.few) forward_by<T, OT, DP, 1, sizeof(T) == 2 ? 4 : 2, 1>(a, p, st);
+  if (f.rw == 1) forward_by<T, OT, DP, 1, sizeof(T) == 2 ? 4 : 2, 1>(a, p, st);
+  else if (f.rw == 2) forward_by<T, OT, DP, 2, 2, 1>(a, p, st);
   else forward_by<T, OT, DP, 4, 1, sizeof(T) == 2 ? 2 : 1>(a, p, st);
 }
 
-// The backward's pass over key tiles: 64 keys a block, and the blocks that share
-// a tile's rows.
+// The backward's pass over key tiles: KW waves of 32 keys by QW of rows that share
+// them, QT times 32 rows each a stage.
+template <typename T, int DP>
+struct BwdShape {
+  static constexpr int KW = sizeof(T) == 2 && DP == 128 ? 4 : 2, QW = 4 / KW, QT = 2 / QW, BK = 32 * KW, BQ = 64;
+};
+int64_t bwd_keys(const lora_attention* a) { return a->dtype == LORA_BF16 && a->head_dim > 64 ? 128 : 64; }
+// Blocks that share a key tile's rows: enough for causal tiles, whose rows differ
+// by the length of the sequence, to even out over the chip.
 struct BwdPlan {
   int64_t tiles, splits;
 };
-constexpr int64_t kBwdKeys = 64, kBwdRows = 64;
 BwdPlan bwd_plan(const lora_attention* a) {
   const int64_t group = a->heads / a->kv_heads;
   BwdPlan b;
-  b.tiles = tile_count(a->k_tokens, 1, a->seqs, kBwdKeys);
-  b.splits = clampi(cdiv(2 * kCUs, b.tiles * a->kv_heads), 1,
-                    clampi(a->q_tokens * group / a->seqs / (2 * kBwdRows), 1, 64));
+  b.tiles = tile_count(a->k_tokens, 1, a->seqs, bwd_keys(a));
+  const int64_t want = (a->head_dim > 64 ? 2 : 4) * kCUs;
+  b.splits = clampi(cdiv(want, b.tiles * a->kv_heads), 1, clampi(a->q_tokens * group / a->seqs / 128, 1, 32));
   return b;
 }
 // The backward's workspace: row statistics, dO rounded to bf16, split sums.
@@ -162,16 +171,20 @@ BwdSpace bwd_space(const lora_attention* a) {
 
 template <typename T, typename OT, int DP>
 void backward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
-  constexpr int W = 4, KT = sizeof(T) == 2 ? 2 : 1;
-  constexpr int QW = 2, QT = (int)kBwdRows / 32 / QW, KW = (int)kBwdKeys / 32;
+  constexpr int KT = sizeof(T) == 2 ? 2 : 1;
+  typedef BwdShape<T, DP> S;
   const BwdSpace w = bwd_space(a);
   p.stat = (float*)ws;
   p.dO16 = (char*)ws + w.dO16;
   p.part = (float*)((char*)ws + w.part);
+  // Two rows' waves a block, which share the keys, where four would leave CUs idle.
+  const bool small = tile_count(a->q_tokens, p.group, a->seqs, 128) * p.kv < kCUs;
   {
-    p.tiles = (int32_t)tile_count(a->q_tokens, p.group, a->seqs, 32 * W);
+    p.tiles = (int32_t)tile_count(a->q_tokens, p.group, a->seqs, small ? 64 : 128);
     prof::Scope ps("attn_dq", a->q_tokens, a->k_tokens, a->heads, 6.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 3));
-    launch_n(attn_dq_kernel<T, OT, DP, W, KT>, dim3((unsigned)(p.tiles * p.kv)), 64 * W, st, ps, p);
+    const dim3 grid((unsigned)(p.tiles * p.kv));
+    if (small) launch_n(attn_dq_kernel<T, OT, DP, 2, 2, 1>, grid, 256u, st, ps, p);
+    else launch_n(attn_dq_kernel<T, OT, DP, 4, 1, KT>, grid, 256u, st, ps, p);
   }
   const BwdPlan b = bwd_plan(a);
   p.tiles = (int32_t)b.tiles;
@@ -179,11 +192,11 @@ void backward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
   const int64_t blocks = b.tiles * p.kv;
   {
     prof::Scope ps("attn_dkv", a->q_tokens, a->k_tokens, a->heads, 8.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 2));
-    launch_n(attn_dkv_kernel<T, OT, DP, KW, QW, QT>, dim3((unsigned)(blocks * b.splits)), 64 * KW * QW, st, ps, p);
+    launch_n(attn_dkv_kernel<T, OT, DP, S::KW, S::QW, S::QT>, dim3((unsigned)(blocks * b.splits)), 256u, st, ps, p);
   }
   if (b.splits > 1) {
     prof::Scope ps("attn_dkv_join", a->k_tokens, a->kv_heads, b.splits, 0.0, 8.0 * b.splits * a->kv_heads * a->k_tokens * DP);
-    launch_n(attn_dkv_join_kernel<OT, DP, (int)kBwdKeys>, dim3((unsigned)blocks), 256u, st, ps, p);
+    launch_n(attn_dkv_join_kernel<OT, DP, S::BK>, dim3((unsigned)blocks, S::BK * DP / 512), 256u, st, ps, p);
   }
 }
 

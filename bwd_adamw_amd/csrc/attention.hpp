@@ -29,13 +29,14 @@ struct AttnArgs {
   const void* dO;               // OT
   void *dQ, *dK, *dV;           // OT
   float* lse;                   // [heads][q_tokens], forward: may be NULL
-  float* stat;                  // backward: [2][kv][q_tokens G] log-sums (powers of two) and delta
+  float* stat;                  // backward: [2][kv][q_tokens G] log-sums (powers of two) and -delta
   void* dO16;                   // backward, bf16 with float32 dO: dO rounded, [kv][q_tokens G][DP]
   float *part, *ml;             // splits: sums [splits][kv][q_tokens G][DP], maximum and weight [..][2]
   const int32_t *qo, *ko, *kl;  // offsets [seqs + 1] and lengths [seqs] or NULL
   int64_t ldq, hq, ldk, hk, ldv, hv, ldo, ho;
   int64_t q_tokens, k_tokens;
-  int32_t seqs, kv, group, dim, causal, tiles, splits;
+  int32_t seqs, kv, group, dim, causal, tiles;
+  int32_t splits;               // blocks that share a tile
   float scale, c;               // c = scale log2 e
 };
 
@@ -243,11 +244,10 @@ LORA_DEV uint32_t cols_at(int r0, int lane) {
     return (uint32_t)(row * (DP * 4) + ((((lane & 31) >> 2) ^ attn_swz<T, DP>(row)) << 4) + ((lane & 3) << 2));
   }
 }
-// acc += (rows from `at`) times the register operand f, both along DP.
+// acc + (rows from `at`) times the register operand f, both along DP.
 template <typename T, int DP>
-LORA_DEV f32x16 mma_rows(lds_char* tile, uint32_t at, const typename Frag<T>::V (&f)[DP / Frag<T>::FK]) {
+LORA_DEV f32x16 mma_rows(lds_char* tile, uint32_t at, const typename Frag<T>::V (&f)[DP / Frag<T>::FK], f32x16 acc = {}) {
   typedef __attribute__((address_space(3))) const typename Frag<T>::V LV;
-  f32x16 acc = {};
 #pragma unroll
   for (int s = 0; s < DP / Frag<T>::FK; ++s)
     acc = Frag<T>::mma(*(LV*)(tile + (at ^ (uint32_t)(s << 5))), f[s], acc);
@@ -324,8 +324,8 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 && CW == 1 ? 2 : 1) vo
   constexpr int NW = RW * CW, BM = 32 * RW, BN = 32 * KT * CW, KS = DP / Frag<T>::FK, DT = DP / 32;
   typedef typename Frag<T>::V V;
   typedef Tile<T, DP, BN, NW> Ti;
-  constexpr int STAGE = 2 * Ti::BYTES;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  constexpr int STAGE = 2 * Ti::BYTES, MERGE = CW > 1 ? NW * (DT * 4096 + 512) : 0;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE > MERGE ? 2 * STAGE : MERGE];
   lds_char* const lds = (lds_char*)smem;
   const int split = (int)(blockIdx.x / p.kv) % p.splits;
   const RowTile rt = attn_row_tile(p, (int)(blockIdx.x / p.kv / p.splits) * p.kv + (int)(blockIdx.x % p.kv), BM);
@@ -420,7 +420,6 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 && CW == 1 ? 2 : 1) vo
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     f32x4* sums = reinterpret_cast<f32x4*>(smem);             // [NW][DT][4][64]
     f32x2* mls = reinterpret_cast<f32x2*>(sums + NW * DT * 256);   // [NW][64]
-    static_assert(NW * DT * 4096 + NW * 512 <= 2 * STAGE, "");
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -504,12 +503,55 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
 // dV).  S and dP are computed in both: 7 products where one pass would take 5,
 // but dQ would then be summed over key tiles in memory, in no fixed order.
 // ---------------------------------------------------------------------------
-template <typename T, typename OT, int DP, int RW, int KT>
-__global__ __launch_bounds__(64 * RW, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(AttnArgs p) {
-  constexpr int BM = 32 * RW, BN = 32 * KT, KS = DP / Frag<T>::FK, DT = DP / 32;
+// The block's sequence and key tile.
+struct KeyTile {
+  AttnSeq s;
+  int k0, kvh;
+};
+LORA_DEV KeyTile attn_key_tile(const AttnArgs& p, int b, int BK) {
+  KeyTile r;
+  r.kvh = b % p.kv;
+  const int t = b / p.kv, i = attn_find(p.ko, p.seqs, p.k_tokens, 1, BK, t);
+  r.s = attn_seq(p, i);
+  r.k0 = __builtin_amdgcn_readfirstlane((t - attn_first(p.ko, p.k_tokens, 1, BK, i)) * BK);
+  r.s.q0 = __builtin_amdgcn_readfirstlane(r.s.q0);
+  r.s.k0 = __builtin_amdgcn_readfirstlane(r.s.k0);
+  r.s.lk = __builtin_amdgcn_readfirstlane(r.s.lk);
+  r.s.lq = __builtin_amdgcn_readfirstlane(r.s.lq);
+  return r;
+}
+
+// Wave (a, 0)'s acc += those of waves (a, 1 .. B - 1), in that order, over LDS.
+template <int DP, int A, int B, int ROOM>
+LORA_DEV void add_waves(f32x16 (&acc)[DP / 32], char* smem, int a, int b, int lane) {
+  constexpr int DT = DP / 32;
+  static_assert(A * DT * 4096 <= ROOM, "");
+  f32x4* sums = reinterpret_cast<f32x4*>(smem) + a * DT * 256 + lane;
+#pragma unroll
+  for (int w = 1; w < B; ++w) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (b == w) {
+#pragma unroll
+      for (int x = 0; x < 4 * DT; ++x)
+        sums[64 * x] = f32x4{acc[x >> 2][4 * (x & 3)], acc[x >> 2][4 * (x & 3) + 1], acc[x >> 2][4 * (x & 3) + 2],
+                             acc[x >> 2][4 * (x & 3) + 3]};
+    }
+    __syncthreads();
+    if (b == 0) {
+#pragma unroll
+      for (int x = 0; x < 4 * DT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[x >> 2][4 * (x & 3) + e] += sums[64 * x][e];
+    }
+  }
+}
+
+template <typename T, typename OT, int DP, int RW, int CW, int KT>
+__global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(AttnArgs p) {
+  constexpr int NW = RW * CW, BM = 32 * RW, BN = 32 * KT * CW, KS = DP / Frag<T>::FK, DT = DP / 32;
   constexpr bool MIXED = !std::is_same_v<T, OT>;
   typedef typename Frag<T>::V V;
-  typedef Tile<T, DP, BN, RW> Ti;
+  typedef Tile<T, DP, BN, NW> Ti;
   constexpr int STAGE = 2 * Ti::BYTES;
   __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
   lds_char* const lds = (lds_char*)smem;
@@ -518,11 +560,12 @@ __global__ __launch_bounds__(64 * RW, sizeof(T) == 2 ? 2 : 1) void attn_dq_kerne
   const int m0 = rt.m0, rows = rt.rows, kvh = rt.kvh;
   if (m0 < 0 || m0 >= rows) return;
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m = m0 + 32 * wave + (lane & 31), mc = min(m, rows - 1);
+  const int rw = wave % RW, cw = wave / RW;
+  const int m = m0 + 32 * rw + (lane & 31), mc = min(m, rows - 1);
   const int tok = mc / p.group, head = kvh * p.group + mc % p.group;
   const int lim = attn_limit(p, sq, tok);
   const int most = attn_limit(p, sq, (min(m0 + BM, rows) - 1) / p.group);
-  const int least = attn_limit(p, sq, min(m0 + 32 * wave, rows - 1) / p.group);
+  const int least = attn_limit(p, sq, min(m0 + 32 * rw, rows - 1) / p.group);
   V qf[KS], df[KS];
   load_frags<T, DP>(qf, (const T*)p.Q + (sq.q0 + tok) * p.ldq + head * p.hq, p.dim, half);
   const OT* dor = (const OT*)p.dO + (sq.q0 + tok) * p.ldo + head * p.ho;
@@ -540,10 +583,10 @@ __global__ __launch_bounds__(64 * RW, sizeof(T) == 2 ? 2 : 1) void attn_dq_kerne
   const float lse = p.lse[head * p.q_tokens + sq.q0 + tok];
   const float lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;   // (no keys: nothing below counts)
   const int64_t R = p.q_tokens * p.group, at = kvh * R + (int64_t)sq.q0 * p.group + m;
-  if (m < rows) {   // for the pass over key tiles
+  if (cw == 0 && m < rows) {   // for the pass over key tiles
     if (half == 0) {
       p.stat[at] = lse2;
-      p.stat[p.kv * R + at] = delta;
+      p.stat[p.kv * R + at] = -delta;
     }
     if constexpr (MIXED) {
 #pragma unroll
@@ -570,19 +613,23 @@ __global__ __launch_bounds__(64 * RW, sizeof(T) == 2 ? 2 : 1) void attn_dq_kerne
     Ti::load(attn_rsrc(vp, vleft), lds + buf * STAGE + Ti::BYTES, wave, va);
     kp += kstep, vp += vstep, kleft -= kstep, vleft -= vstep;
   };
-  const uint32_t rat = rows_at<T, DP>(0, lane), cat = cols_at<T, DP>(0, lane);
-  auto step = [&](int kb, auto B) {
+  const uint32_t rat = rows_at<T, DP>(32 * KT * cw, lane), cat = cols_at<T, DP>(32 * KT * cw, lane);
+  auto step = [&](int k0, auto B) {
     constexpr int buf = decltype(B)::value;
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kb + BN < most) load(buf ^ 1);
+    if (k0 + BN < most) load(buf ^ 1);
+    const int kb = k0 + 32 * KT * cw;
     lds_char* const Ks = lds + buf * STAGE;
     lds_char* const Vs = Ks + Ti::BYTES;
 #pragma unroll
     for (int j = 0; j < KT; ++j) {
       f32x16 s = mma_rows<T, DP>(Ks + 32 * j * Ti::ROWB, rat, qf);
-      const f32x16 dp = mma_rows<T, DP>(Vs + 32 * j * Ti::ROWB, rat, df);
+      f32x16 dp;   // dP - delta: the product's sums start at -delta
 #pragma unroll
-      for (int v = 0; v < 16; ++v) s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], p.c, -lse2)) * (dp[v] - delta);
+      for (int v = 0; v < 16; ++v) dp[v] = -delta;
+      dp = mma_rows<T, DP>(Vs + 32 * j * Ti::ROWB, rat, df, dp);
+#pragma unroll
+      for (int v = 0; v < 16; ++v) s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], p.c, -lse2)) * dp[v];
       if (kb + 32 * j + 32 > least) {   // after the products: what a masked score gives must not count
 #pragma unroll
         for (int v = 0; v < 16; ++v) s[v] = kb + 32 * j + row32(v, lane) >= lim ? 0.0f : s[v];
@@ -596,26 +643,9 @@ __global__ __launch_bounds__(64 * RW, sizeof(T) == 2 ? 2 : 1) void attn_dq_kerne
     step(kb, std::integral_constant<int, 0>{});
     if (kb + BN < most) step(kb + BN, std::integral_constant<int, 1>{});
   }
-  if (m >= rows) return;
+  if constexpr (CW > 1) add_waves<DP, RW, CW, 2 * STAGE>(dq, smem, rw, cw, lane);
+  if (cw > 0 || m >= rows) return;
   store_row<DP>((OT*)p.dQ + (sq.q0 + tok) * p.ldq + head * p.hq, dq, p.scale, p.dim, half);
-}
-
-// The block's sequence and key tile.
-struct KeyTile {
-  AttnSeq s;
-  int k0, kvh;
-};
-LORA_DEV KeyTile attn_key_tile(const AttnArgs& p, int b, int BK) {
-  KeyTile r;
-  r.kvh = b % p.kv;
-  const int t = b / p.kv, i = attn_find(p.ko, p.seqs, p.k_tokens, 1, BK, t);
-  r.s = attn_seq(p, i);
-  r.k0 = __builtin_amdgcn_readfirstlane((t - attn_first(p.ko, p.k_tokens, 1, BK, i)) * BK);
-  r.s.q0 = __builtin_amdgcn_readfirstlane(r.s.q0);
-  r.s.k0 = __builtin_amdgcn_readfirstlane(r.s.k0);
-  r.s.lk = __builtin_amdgcn_readfirstlane(r.s.lk);
-  r.s.lq = __builtin_amdgcn_readfirstlane(r.s.lq);
-  return r;
 }
 
 // dK and dV.  A block's KW waves hold 32 keys each in registers, times QW that
@@ -623,7 +653,7 @@ LORA_DEV KeyTile attn_key_tile(const AttnArgs& p, int b, int BK) {
 // neighbouring tokens) with their log-sums and deltas.  p.splits blocks share a
 // key tile's stages where there are few tiles.
 template <typename T, typename OT, int DP, int KW, int QW, int QT>
-__global__ __launch_bounds__(64 * KW * QW, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(AttnArgs p) {
+__global__ __launch_bounds__(64 * KW * QW, DP == 64 && sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(AttnArgs p) {
   constexpr int NW = KW * QW, BK = 32 * KW, BQ = 32 * QW * QT, KS = DP / Frag<T>::FK, DT = DP / 32;
   constexpr bool MIXED = !std::is_same_v<T, OT>;
   typedef typename Frag<T>::V V;
@@ -702,17 +732,21 @@ __global__ __launch_bounds__(64 * KW * QW, sizeof(T) == 2 ? 2 : 1) void attn_dkv
       const int r0 = 32 * (QT * qw + j), mb = st * BQ + r0;
       if (mb + 31 < some) continue;
       lds_char* const stat = Ds + Ti::BYTES + 4 * (r0 + 4 * half);
-      f32x16 s = mma_rows<T, DP>(Qs + 32 * j * Ti::ROWB, rat, kf);
-      f32x16 ds = mma_rows<T, DP>(Ds + 32 * j * Ti::ROWB, rat, vf);
+      f32x4 ls[4];
+      f32x16 ds;   // dP - delta: the product's sums start at -delta
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f32x4 ls = *(LV*)(stat + 32 * q), de = *(LV*)(stat + SB + 32 * q);
+        ls[q] = *(LV*)(stat + 32 * q);
+        const f32x4 de = *(LV*)(stat + SB + 32 * q);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int v = 4 * q + e;
-          s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], p.c, -ls[e]));
-          ds[v] = s[v] * (ds[v] - de[e]);
-        }
+        for (int e = 0; e < 4; ++e) ds[4 * q + e] = de[e];
+      }
+      f32x16 s = mma_rows<T, DP>(Qs + 32 * j * Ti::ROWB, rat, kf);
+      ds = mma_rows<T, DP>(Ds + 32 * j * Ti::ROWB, rat, vf, ds);
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], p.c, -ls[v >> 2][v & 3]));
+        ds[v] *= s[v];
       }
       if (mb < all) {
 #pragma unroll
@@ -732,29 +766,9 @@ __global__ __launch_bounds__(64 * KW * QW, sizeof(T) == 2 ? 2 : 1) void attn_dkv
     step(st, std::integral_constant<int, 0>{});
     if (st + 1 < st1) step(st + 1, std::integral_constant<int, 1>{});
   }
-  if constexpr (QW > 1) {   // added up in wave order, dK then dV
-    static_assert(KW * DT * 4096 <= 2 * STAGE, "");
-    f32x4* sums = reinterpret_cast<f32x4*>(smem) + kw * DT * 256 + lane;
-#pragma unroll
-    for (int w = 1; w < QW; ++w)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        f32x16(&acc)[DT] = k == 0 ? dk : dv;
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (qw == w) {
-#pragma unroll
-          for (int x = 0; x < 4 * DT; ++x)
-            sums[64 * x] = f32x4{acc[x >> 2][4 * (x & 3)], acc[x >> 2][4 * (x & 3) + 1], acc[x >> 2][4 * (x & 3) + 2],
-                                 acc[x >> 2][4 * (x & 3) + 3]};
-        }
-        __syncthreads();
-        if (qw == 0) {
-#pragma unroll
-          for (int x = 0; x < 4 * DT; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[x >> 2][4 * (x & 3) + e] += sums[64 * x][e];
-        }
-      }
+  if constexpr (QW > 1) {
+    add_waves<DP, KW, QW, 2 * STAGE>(dk, smem, kw, qw, lane);
+    add_waves<DP, KW, QW, 2 * STAGE>(dv, smem, kw, qw, lane);
     if (qw > 0) return;
   }
   if (key >= sq.lk) return;
@@ -768,22 +782,22 @@ __global__ __launch_bounds__(64 * KW * QW, sizeof(T) == 2 ? 2 : 1) void attn_dkv
   store_row<DP>((OT*)p.dV + (sq.k0 + key) * p.ldv + kvh * p.hv, dv, 1.0f, p.dim, half);
 }
 
-// dK and dV from the splits' sums, in split order: DP / 2 threads a key.
+// dK and dV from the splits' sums, in split order: DP / 2 threads a key,
+// blockIdx.y the keys of the tile in turn.
 template <typename OT, int DP, int BK>
 __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs p) {
+  constexpr int KEYS = 256 / (DP / 2);
   const KeyTile kt = attn_key_tile(p, (int)blockIdx.x, BK);
-  if (kt.k0 < 0 || kt.k0 >= kt.s.lk) return;
+  const int r = KEYS * blockIdx.y + threadIdx.x / (DP / 2);
+  if (kt.k0 < 0 || r >= BK || kt.k0 + r >= kt.s.lk) return;
   const int x = 4 * (threadIdx.x % (DP / 2)), d = x % DP;
-  const int64_t step = p.k_tokens * p.kv * 2 * DP;
-  for (int r = threadIdx.x / (DP / 2); r < BK && kt.k0 + r < kt.s.lk; r += 256 / (DP / 2)) {
-    const int64_t key = kt.s.k0 + kt.k0 + r;
-    const f32x4 o = sum_parts4(p.part, step, p.splits, (kt.kvh * p.k_tokens + key) * 2 * DP + x);
-    if (d >= p.dim) continue;
-    if (x < DP)
-      store_4((OT*)p.dK + key * p.ldk + kt.kvh * p.hk + d, o[0] * p.scale, o[1] * p.scale, o[2] * p.scale, o[3] * p.scale);
-    else
-      store_4((OT*)p.dV + key * p.ldv + kt.kvh * p.hv + d, o[0], o[1], o[2], o[3]);
-  }
+  const int64_t key = kt.s.k0 + kt.k0 + r;
+  const f32x4 o = sum_parts4(p.part, p.k_tokens * p.kv * 2 * DP, p.splits, (kt.kvh * p.k_tokens + key) * 2 * DP + x);
+  if (d >= p.dim) return;
+  if (x < DP)
+    store_4((OT*)p.dK + key * p.ldk + kt.kvh * p.hk + d, o[0] * p.scale, o[1] * p.scale, o[2] * p.scale, o[3] * p.scale);
+  else
+    store_4((OT*)p.dV + key * p.ldv + kt.kvh * p.hv + d, o[0], o[1], o[2], o[3]);
 }
 
 }  // namespace lora
