@@ -120,7 +120,7 @@ void forward_by(const lora_attention* a, const AttnArgs& p, hipStream_t st) {
   }
   if (p.splits > 1) {
     prof::Scope ps("attn_join", a->q_tokens, a->heads, p.splits, 0.0, 4.0 * p.splits * a->heads * a->q_tokens * DP);
-    launch_n(attn_join_kernel<OT, DP, 32 * RW>, dim3((unsigned)blocks), 256u, st, ps, p);
+    launch_n(attn_join_kernel<OT, DP, 32 * RW>, dim3((unsigned)blocks, 32 * RW * DP / 1024), 256u, st, ps, p);
   }
 }
 template <typename T, typename OT, int DP>

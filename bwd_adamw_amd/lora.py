@@ -946,12 +946,13 @@ def make_heads(tokens, heads, head_dim, x_dtype=torch.float32, y_dtype=None, nor
     return out
 
 
-def _strided(t, name, tokens, heads, dim, ld, h, dtype):
+def _strided(t, name, i, tokens, heads, dim, ld, h, dtype):
     """Device pointer of heads whose tokens are ld and heads h elements apart:
     a [tokens, heads, dim] tensor of those strides, or (where the heads of a
     token lie together) [tokens, heads * dim]."""
     if t is None:
         return None
+    name = name if i is None else f"{name}[{i}]"
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -969,22 +970,34 @@ def _strided(t, name, tokens, heads, dim, ld, h, dtype):
     return t.data_ptr()
 
 
-def _head_ptrs(heads, ts, name, side):
+def _head_ptr(t, name, i, tokens, heads, dim, ld, h, dtype):
+    """_strided, in few steps for the usual tensors (a token's call is host
+    time: the checks above take 2 us a tensor)."""
+    if type(t) is torch.Tensor and t.is_cuda and _ACT_DTYPES.get(t.dtype) == dtype:
+        shape, st = t.shape, t.stride()
+        if (shape == (tokens, heads, dim) and st == (ld, h, 1)) or \
+                (h == dim and shape == (tokens, heads * dim) and st == (ld, 1)):
+            return t.data_ptr()
+    return _strided(t, name, i, tokens, heads, dim, ld, h, dtype)
+
+
+def _head_ptrs(heads, ts, name, x):
     if ts is None:
         return None
     if len(ts) != len(heads):
         raise ValueError(f"{name} has {len(ts)} entries for {len(heads)} sets of heads")
-    return (C.c_void_p * len(ts))(*[
-        _strided(t, f"{name}[{i}]", h.tokens, h.heads, h.head_dim,
-                 *((h.ldx, h.hx, h.x_dtype) if side == "x" else (h.ldy, h.hy, h.y_dtype)))
-        for i, (t, h) in enumerate(zip(ts, heads))])
+    out = (C.c_void_p * len(ts))()
+    for i, d in enumerate(heads):
+        out[i] = _head_ptr(ts[i], name, i, d.tokens, d.heads, d.head_dim,
+                           *((d.ldx, d.hx, d.x_dtype) if x else (d.ldy, d.hy, d.y_dtype)))
+    return out
 
 
 def lora_heads_forward(heads, X, Y, positions=None, stream=None):
     """Y[i] = the heads X[i], normed and rotated, for each set of `heads` (one
     to four of the same tokens); positions [tokens] int32."""
     arr = (LoraHeads * len(heads))(*heads)
-    rc = lib().lora_heads_forward(len(heads), arr, _head_ptrs(heads, X, "X", "x"), _head_ptrs(heads, Y, "Y", "y"),
+    rc = lib().lora_heads_forward(len(heads), arr, _head_ptrs(heads, X, "X", True), _head_ptrs(heads, Y, "Y", False),
                                   _device_ints(positions, "positions", heads[0].tokens if len(heads) else 0),
                                   _stream(stream))
     _check("lora_heads_forward", rc)
@@ -1008,8 +1021,8 @@ def lora_heads_backward(heads, X, dY, dX=None, dgamma=None, positions=None, accu
         need = int(lib().lora_heads_workspace_bytes(len(heads), arr))
         if need:
             ws = _own_ws(need, dY[0].device, stream)
-    rc = lib().lora_heads_backward(len(heads), arr, _head_ptrs(heads, X, "X", "x"), _head_ptrs(heads, dY, "dY", "y"),
-                                   _head_ptrs(heads, dX, "dX", "x"), dg,
+    rc = lib().lora_heads_backward(len(heads), arr, _head_ptrs(heads, X, "X", True), _head_ptrs(heads, dY, "dY", False),
+                                   _head_ptrs(heads, dX, "dX", True), dg,
                                    _device_ints(positions, "positions", heads[0].tokens if len(heads) else 0),
                                    1 if accumulate else 0, _ptr(ws, "ws", None),
                                    0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
@@ -1040,19 +1053,21 @@ def lora_attention_workspace_bytes(at: LoraAttention, backward=False) -> int:
     return int(lib().lora_attention_workspace_bytes(C.byref(at), 1 if backward else 0))
 
 
-def _attn_ptr(at, t, name, of, out):
-    """Device pointer of a tensor laid out like Q, K, V or O."""
-    n, h = (at.q_tokens, at.heads) if of in "qo" else (at.k_tokens, at.kv_heads)
-    return _strided(t, name, n, h, at.head_dim, getattr(at, "ld" + of), getattr(at, "h" + of),
-                    at.out_dtype if out else at.dtype)
+def _attn_ptrs(at, ts):
+    """Device pointers of tensors laid out like Q, K, V or O: (tensor, name,
+    whose strides, whether of out_dtype)."""
+    q, k, d, io = (at.q_tokens, at.heads), (at.k_tokens, at.kv_heads), at.head_dim, (at.dtype, at.out_dtype)
+    lay = {"q": (*q, d, at.ldq, at.hq), "k": (*k, d, at.ldk, at.hk), "v": (*k, d, at.ldv, at.hv),
+           "o": (*q, d, at.ldo, at.ho)}
+    return [_head_ptr(t, name, None, *lay[of], io[out]) for t, name, of, out in ts]
 
 
 def lora_attention_forward(at: LoraAttention, Q, K, V, O, lse=None, ws=None, stream=None):
     """O = attention of Q over K and V; lse [heads, q_tokens] float32 receives
     what the backward needs.  `ws` is taken from torch's allocator when one is
     needed and it is None."""
-    ptrs = [_attn_ptr(at, Q, "Q", "q", 0), _attn_ptr(at, K, "K", "k", 0), _attn_ptr(at, V, "V", "v", 0),
-            _attn_ptr(at, O, "O", "o", 1), _sized(lse, "lse", at.heads * at.q_tokens)]
+    ptrs = _attn_ptrs(at, ((Q, "Q", "q", 0), (K, "K", "k", 0), (V, "V", "v", 0), (O, "O", "o", 1)))
+    ptrs.append(_sized(lse, "lse", at.heads * at.q_tokens))
     if ws is None:
         need = int(lib().lora_attention_workspace_bytes(C.byref(at), 0))
         if need:
@@ -1065,10 +1080,9 @@ def lora_attention_forward(at: LoraAttention, Q, K, V, O, lse=None, ws=None, str
 def lora_attention_backward(at: LoraAttention, Q, K, V, O, dO, lse, dQ, dK, dV, ws=None, stream=None):
     """Gradients of lora_attention_forward from dO; `ws` is taken from torch's
     allocator when None."""
-    ptrs = [_attn_ptr(at, Q, "Q", "q", 0), _attn_ptr(at, K, "K", "k", 0), _attn_ptr(at, V, "V", "v", 0),
-            _attn_ptr(at, O, "O", "o", 1), _attn_ptr(at, dO, "dO", "o", 1),
-            _sized(lse, "lse", at.heads * at.q_tokens), _attn_ptr(at, dQ, "dQ", "q", 1),
-            _attn_ptr(at, dK, "dK", "k", 1), _attn_ptr(at, dV, "dV", "v", 1)]
+    ptrs = _attn_ptrs(at, ((Q, "Q", "q", 0), (K, "K", "k", 0), (V, "V", "v", 0), (O, "O", "o", 1), (dO, "dO", "o", 1),
+                           (dQ, "dQ", "q", 1), (dK, "dK", "k", 1), (dV, "dV", "v", 1)))
+    ptrs.insert(5, _sized(lse, "lse", at.heads * at.q_tokens))
     if ws is None:
         ws = _own_ws(max(16, int(lib().lora_attention_workspace_bytes(C.byref(at), 1))), dQ.device, stream)
     rc = lib().lora_attention_backward(C.byref(at), *ptrs, _ptr(ws, "ws", None), ws.numel() * ws.element_size(),
