@@ -255,24 +255,32 @@ LORA_DEV f32x16 mma_rows(lds_char* tile, uint32_t at, const typename Frag<T>::V 
 }
 // acc[dt] += (32 rows from `at`)^T x, x a product's result with the same rows
 // down its registers.  bf16: values 8 u .. 8 u + 7 of lane half h are rows
-// 16 u + 4 h + 0..3 and 16 u + 8 + 4 h + 0..3, the transpose reads' order.
-template <typename T, int DP>
+// 16 u + 4 h + 0..3 and 16 u + 8 + 4 h + 0..3, the transpose reads' order.  TWICE
+// adds what the rounding of x to bf16 left, rounded in its turn.
+template <typename T, int DP, bool TWICE = false>
 LORA_DEV void mma_cols(f32x16 (&acc)[DP / 32], lds_char* tile, uint32_t at, const f32x16& x) {
   constexpr int ROWB = DP * (int)sizeof(T);
   if constexpr (sizeof(T) == 2) {
     typedef __attribute__((address_space(3))) attn_s4 LV;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      u32x4 b;
+      u32x4 b, low;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) b[e] = cvt_bf16x2(x[8 * u + 2 * e], x[8 * u + 2 * e + 1]);
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = x[8 * u + 2 * e], x1 = x[8 * u + 2 * e + 1];
+        b[e] = cvt_bf16x2(x0, x1);
+        if constexpr (TWICE)
+          low[e] = cvt_bf16x2(x0 - __uint_as_float(b[e] << 16), x1 - __uint_as_float(b[e] & 0xffff0000u));
+      }
 #pragma unroll
       for (int dt = 0; dt < DP / 32; ++dt) {
         const attn_s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LV*)(tile + 16 * u * ROWB + (at ^ (uint32_t)(dt << 6))));
         const attn_s4 hi =
             __builtin_amdgcn_ds_read_tr16_b64_v4i16((LV*)(tile + (16 * u + 8) * ROWB + (at ^ (uint32_t)(dt << 6) ^ 32u)));
         const u32x2 a0 = __builtin_bit_cast(u32x2, lo), a1 = __builtin_bit_cast(u32x2, hi);
-        acc[dt] = mfma32x32x16_bf16(u32x4{a0[0], a0[1], a1[0], a1[1]}, b, acc[dt]);
+        const u32x4 a = u32x4{a0[0], a0[1], a1[0], a1[1]};
+        acc[dt] = mfma32x32x16_bf16(a, b, acc[dt]);
+        if constexpr (TWICE) acc[dt] = mfma32x32x16_bf16(a, low, acc[dt]);
       }
     }
   } else {
@@ -741,7 +749,7 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 ? 2 : 1) void attn_dq_
 #pragma unroll
         for (int v = 0; v < 16; ++v) s[v] = kb + 32 * j + row32(v, lane) >= lim ? 0.0f : s[v];
       }
-      mma_cols<T, DP>(dq, Ks + 32 * j * Ti::ROWB, cat, s);
+      mma_cols<T, DP, true>(dq, Ks + 32 * j * Ti::ROWB, cat, s);
     }
   };
   if (most > 0) load(0);

@@ -1,12 +1,14 @@
 """An optimizer update over an 8-bit base, with the norms before its layers.
 
-    python -m bwd_adamw_amd.fp8_step [--layers 36] [--tokens 4096] [--steps 5]
+    python -m bwd_adamw_amd.fp8_step [--layers 36] [--tokens 4096] [--steps 5] [--attention [SEQUENCES]]
 
 Adapters on Qwen3-4B-shaped layers whose frozen weights are e4m3 with a scale
 for each 128 x 128 block: an RMS norm before each group of projections that
 read the residual stream, the groups' forward and backward on 8-bit products,
 the norms' backward over the summed gradients of their projections, and the
-orthogonalised update of the factors.  Inputs are seeded and synthetic.
+orthogonalised update of the factors.  With --attention the query and key heads
+are normed and rotated, and wo reads their causal attention over that many
+packed sequences (1).  Inputs are seeded and synthetic.
 """
 
 from __future__ import annotations
@@ -25,8 +27,13 @@ from . import workloads as WL
 NORMED = (0, 2)
 
 
-def build(cfg, device="cuda", **kw):
-    """(trainer, slot, chunks) of `cfg` with 8-bit weights and norms."""
+#: Key heads and head size of the Qwen3-4B-shaped layers, and the base of their angles.
+KV_HEADS, HEAD_DIM, ROPE_BASE = 8, 128, 1e6
+
+
+def build(cfg, device="cuda", sequences=0, **kw):
+    """(trainer, slot, chunks) of `cfg` with 8-bit weights and norms, and with
+    attention over `sequences` equal parts of the chunk."""
     cfg = dataclasses.replace(cfg, w_dtype="fp8", optimizer="muon",
                               name=cfg.name.replace("bf16", "fp8"))
     weights, A, B, chunk = {}, {}, {}, {}
@@ -41,7 +48,15 @@ def build(cfg, device="cuda", **kw):
     dims = {pj.x_group: pj.in_dim for pj in cfg.projections}
     norms = {(l, g): ("rms", 1e-6, torch.ones(dims[g], device=device), None)
              for l in range(cfg.layers) for g in NORMED if g in dims}
-    model = S.FrozenModel(cfg, weights, norms)
+    attention = {}
+    if sequences:
+        ones = torch.ones(HEAD_DIM, device=device)
+        spec = S.AttentionSpec(dict((p.ordinal, p.out_dim) for p in cfg.projections)[0] // HEAD_DIM, KV_HEADS, HEAD_DIM,
+                               L.rope_freqs(HEAD_DIM, ROPE_BASE, device), True, ones, ones)
+        attention = {l: spec for l in range(cfg.layers)}
+        chunk["offsets"] = torch.arange(sequences + 1, device=device).mul_(cfg.tokens).div_(
+            sequences, rounding_mode="floor").int()
+    model = S.FrozenModel(cfg, weights, norms, attention)
     slot = S.Slot(cfg, model, A, B, cfg.seeds[0], device)
     return S.Trainer(cfg, model, device=device, **kw), slot, [chunk]
 
@@ -51,9 +66,10 @@ def main():
     ap.add_argument("--layers", type=int, default=36)
     ap.add_argument("--tokens", type=int, default=4096)
     ap.add_argument("--steps", type=int, default=5)
+    ap.add_argument("--attention", type=int, nargs="?", const=1, default=0, metavar="SEQUENCES")
     args = ap.parse_args()
     cfg = WL.get_config(4).shrink(layers=args.layers, tokens=args.tokens)
-    trainer, slot, chunks = build(cfg)
+    trainer, slot, chunks = build(cfg, sequences=args.attention)
     for k in range(2 + args.steps):
         if k == 2:
             torch.cuda.synchronize()

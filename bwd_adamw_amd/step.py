@@ -4,7 +4,8 @@ Order of one update of a slot ("4.3. Training Guide", "Gradient
 accumulation"; "8. LoRA Fundamentals", "The training loop"):
 
   for each accumulation chunk g:
-      forward of every adapted linear, layers 0..L-1
+      forward of every adapted linear, layers 0..L-1 (where the model says
+      so, with the norm before a group, and the attention between wv and wo)
       backward of every adapted linear, layers L-1..0 (gradients summed
       into the slot's arena; chunk 0 overwrites, later chunks add)
   prepare: global norm in double, non-finite veto, one combined scale
@@ -29,7 +30,7 @@ import torch
 from . import lora as L
 from .workloads import LoraConfig
 
-__all__ = ["FrozenModel", "Slot", "Trainer"]
+__all__ = ["AttentionSpec", "FrozenModel", "Slot", "Trainer"]
 
 
 def _w_desc(W):
@@ -40,17 +41,47 @@ def _w_desc(W):
     return (L.BF16 if W.dtype == torch.bfloat16 else L.F32), W.data_ptr()
 
 
+@dataclass(frozen=True, eq=False)
+class AttentionSpec:
+    """The attention between a layer's wq, wk, wv and its wo: the heads of the
+    three outputs (queries and keys normed over the head with q_gamma and
+    k_gamma where qk_norm is set, and rotated by freqs [pairs] float64 as
+    lora.rope_freqs gives them, None: not rotated), and causal attention over
+    the sequences of a chunk.  dtype is that of its products."""
+    heads: int
+    kv_heads: int
+    head_dim: int
+    freqs: torch.Tensor | None = None
+    qk_norm: bool = False
+    q_gamma: torch.Tensor | None = None
+    k_gamma: torch.Tensor | None = None
+    eps: float = 1e-6
+    interleaved: bool = False
+    scale: float | None = None
+    dtype: torch.dtype = torch.bfloat16
+
+
 class FrozenModel:
     """The frozen weights of every adapted linear, keyed (layer, proj ordinal):
     float32 or bfloat16 tensors, block-quantized QWeights or 8-bit Fp8Weights.
     norms, keyed (layer, x_group), are the frozen norms whose outputs the
     groups read: (kind, eps, gamma, beta or None) as make_norm takes them.
-    A group with a norm takes the norm's input as its X."""
+    A group with a norm takes the norm's input as its X.
 
-    def __init__(self, cfg: LoraConfig, weights: dict, norms: dict | None = None):
+    attention maps a layer to its AttentionSpec: wo then reads the attention of
+    the outputs of wq, wk and wv (ordinals 0 to 3), whose gradients come from
+    wo's; a chunk's X of wo and dY of the three are not read (None will do).  The
+    chunk's sequences are chunk["offsets"] (a list or tensor of sequences + 1
+    numbers from 0 to the chunk's tokens; one sequence without it) and its
+    tokens' positions chunk["positions"] (int32 [tokens] on the GPU; from 0 in
+    each sequence without it)."""
+
+    def __init__(self, cfg: LoraConfig, weights: dict, norms: dict | None = None,
+                 attention: dict | None = None):
         self.cfg = cfg
         self.W = weights
         self.norms = norms or {}
+        self.attention = attention or {}
         self.keys = sorted(weights)
         self.shape = {}
         for key in self.keys:
@@ -126,6 +157,43 @@ class _Norm:
     part: torch.Tensor | None = None   # dH of a further group
 
 
+class _Attention:
+    """Buffers and descriptors of one layer's attention in the trainer."""
+
+    def __init__(self, spec: AttentionSpec, keys, Y, dX, T, device):
+        self.spec, self.T = spec, T
+        self.Y, self.dO = [Y[k] for k in keys[:3]], dX[keys[3]]
+        h, kv, d = spec.heads, spec.kv_heads, spec.head_dim
+        new = lambda n, dt: torch.empty(T, n * d, device=device, dtype=dt)
+        f32 = torch.float32
+        self.q, self.k = new(h, spec.dtype), new(kv, spec.dtype)
+        # values are taken as they are where the products are float32
+        self.v = self.Y[2] if spec.dtype == f32 else new(kv, spec.dtype)
+        self.O, self.lse = new(h, f32), torch.empty(h, T, device=device)
+        self.dY = [new(n, f32) for n in (h, kv, kv)]   # gradients of Y, first of q, k and v
+        kw = dict(eps=spec.eps, norm=spec.qk_norm, freqs=spec.freqs, interleaved=spec.interleaved)
+        sets = ((h, spec.q_gamma), (kv, spec.k_gamma))
+        self.fwd = [L.make_heads(T, n, d, f32, spec.dtype, gamma=g, **kw) for n, g in sets]
+        self.bwd = [L.make_heads(T, n, d, f32, f32, gamma=g, **kw) for n, g in sets]
+        if self.v is not self.Y[2]:
+            self.fwd.append(L.make_heads(T, kv, d, f32, spec.dtype, norm=False))
+
+    def packed(self, offsets):
+        s = self.spec
+        return L.make_attention(self.T, self.T, s.heads, s.kv_heads, s.head_dim, offsets, offsets, dtype=s.dtype,
+                                out_dtype=torch.float32, scale=s.scale)
+
+    def forward(self, at, positions, ws, stream):
+        out = [self.q, self.k, self.v][:len(self.fwd)]
+        L.lora_heads_forward(self.fwd, self.Y[:len(self.fwd)], out, positions, stream=stream)
+        L.lora_attention_forward(at, self.q, self.k, self.v, self.O, self.lse, ws=ws, stream=stream)
+
+    def backward(self, at, positions, ws, stream):
+        L.lora_attention_backward(at, self.q, self.k, self.v, self.O, self.dO, self.lse, *self.dY, ws=ws, stream=stream)
+        # in place: what norm and rotation leave of the gradients of q and k
+        L.lora_heads_backward(self.bwd, self.Y[:2], self.dY[:2], self.dY[:2], None, positions, stream=stream)
+
+
 @dataclass
 class StepStats:
     norm: float
@@ -154,10 +222,10 @@ class Trainer:
         self.T = cfg.tokens if tokens is None else int(tokens)
         # Slots over one W run their frozen products stacked (one pass over W
         # per product) when the library can: bf16 or quantized W and whole
-        # 256-row tiles.  Norms have one set of buffers: slots take turns.
+        # 256-row tiles.  Norms and attention have one set of buffers: slots take turns.
         self.nslots = int(slots)
         self.stack_slots = (self.nslots > 1 and cfg.w_dtype not in ("f32", "fp8")
-                            and self.T % 256 == 0 and not model.norms)
+                            and self.T % 256 == 0 and not model.norms and not model.attention)
         self.scale = L.lora_scaling(cfg.alpha, cfg.rank, cfg.scaling == "rslora")
         self.device = device
         f32 = dict(device=device, dtype=torch.float32)
@@ -219,6 +287,14 @@ class Trainer:
                 nm.part = torch.empty_like(nm.dH)
         # dH[(layer, x_group)]: gradient of a norm's input after forward_backward
         self.dH = {at: nm.dH for at, nm in self.norms.items()}
+        # Attention between the groups of wq, wk, wv and wo's.  One sequence needs
+        # the largest workspace: its keys and rows are dealt to most blocks.
+        self.attention, self._before, self._after = {}, {}, {}
+        if model.attention:
+            self._one = torch.tensor([0, self.T], device=device, dtype=torch.int32)
+        for layer, spec in model.attention.items():
+            self.attention[layer] = at = self._attention(layer, spec)
+            ws = max(ws, *(L.lora_attention_workspace_bytes(at.packed(self._one), b) for b in (False, True)))
         self.ws = torch.empty(max(ws, 256), device=device, dtype=torch.uint8)
         # Streams beyond the current one (default priority), each with a
         # workspace; no more streams than units to spread (layer groups; layers
@@ -228,9 +304,14 @@ class Trainer:
         self.side = [torch.cuda.Stream(device=device) for _ in range(nstreams - 1)]
         self.side_ws = [torch.empty(max(ws, 256), device=device, dtype=torch.uint8)
                         for _ in self.side]
-        # Stream of each group, round robin; the groups of one norm share one.
-        self._on = [(self.normed[gi].groups[0] if gi in self.normed else gi) % nstreams
-                    for gi in range(len(self.groups))]
+        # Stream of each group, round robin; the groups of one norm share one, and
+        # so do those before and after an attention.
+        first = list(range(len(self.groups)))
+        for tie in [nm.groups for nm in self.norms.values()] + [at.groups for at in self.attention.values()]:
+            old = {first[gi] for gi in tie}
+            first = [min(old) if f in old else f for f in first]
+        rank = {f: i for i, f in enumerate(sorted(set(first)))}
+        self._on = [rank[f] % nstreams for f in first]
         self._calls = {}   # (id(slot), group index) -> (slot, stream handle, norms, GroupCall)
         self._refresh = {}  # (streams, slot ids) -> (slots, [(stream, linears, norms)])
         self.d_scale = torch.zeros(1, **f32)
@@ -241,6 +322,44 @@ class Trainer:
             raise ValueError(f"unknown optimizer {cfg.optimizer!r}")
 
     # ------------------------------------------------------------------
+    def _attention(self, layer, spec: AttentionSpec) -> _Attention:
+        """The attention of a layer, placed after the last group of wq, wk and
+        wv (in _after) and before wo's (in _before)."""
+        keys = [(layer, o) for o in range(4)]
+        h, kv, d = spec.heads, spec.kv_heads, spec.head_dim
+        want = [(None, h * d), (None, kv * d), (None, kv * d), (h * d, None)]
+        for k, (K, N) in zip(keys, want):
+            if k not in self.model.shape:
+                raise ValueError(f"attention in layer {layer}: the model has no projection {k}")
+            if (K or self.model.shape[k][0], N or self.model.shape[k][1]) != self.model.shape[k]:
+                raise ValueError(f"attention in layer {layer}: projection {k} is {self.model.shape[k]}, "
+                                 f"{h} and {kv} heads of {d} need {(K, N)}")
+        of = {k: gi for gi, g in enumerate(self.groups) for k in g}
+        if self.groups[of[keys[3]]] != [keys[3]] or of[keys[3]] in self.normed:
+            raise ValueError(f"attention in layer {layer}: projection {keys[3]} must have its input to itself")
+        at = _Attention(spec, keys, self.Y, self.dX, self.T, self.device)
+        self._after[max(of[k] for k in keys[:3])] = at
+        self._before[of[keys[3]]] = at
+        at.groups = [of[k] for k in keys]
+        at.grad = dict(zip(keys[:3], at.dY))
+        return at
+
+    def _sequences(self, chunk):
+        """Offsets and positions of a chunk's sequences on the GPU.  Every token
+        has to be in one: the rows of others would be left as they were."""
+        off, pos = chunk.get("offsets"), chunk.get("positions")
+        if off is None:
+            off = self._one
+        else:
+            at = torch.as_tensor(off).flatten().tolist()
+            if len(at) < 2 or at[0] != 0 or at[-1] != self.T or any(a > b for a, b in zip(at, at[1:])):
+                raise ValueError(f"a chunk's offsets must lead from 0 to its {self.T} tokens without a step back")
+            off = torch.tensor(at, device=self.device, dtype=torch.int32)
+        if pos is None:
+            rows = torch.arange(self.T, device=self.device, dtype=torch.int32)
+            pos = rows - off[torch.searchsorted(off, rows, right=True) - 1]
+        return off, pos
+
     def _linear(self, key, slot, dora=False, norms_only=False):
         W = self.model.W[key]
         K, N = self.model.shape[key]
@@ -344,27 +463,37 @@ class Trainer:
         the projections of a layer that share X go through the group calls."""
         cfg = self.cfg
         p = float(cfg.dropout)
+        seqs = [self._sequences(c) for c in chunks] if self.attention else None
         streams, wss = self._fork()
         ng = len(self.groups)
         calls = [self._group_call(slot, gi, streams[q], wss[q]) for gi, q in enumerate(self._on)]
+        grad = {k: t for at in self.attention.values() for k, t in at.grad.items()}
         for g, chunk in enumerate(chunks):
             dr = [None] * ng
             if p > 0:
                 dr = [calls[gi].dropouts([L.make_dropout(slot.seed, slot.k, g, k[0], k[1], p)
                                           for k in keys])
                       for gi, keys in enumerate(self.groups)]
+            packed = {id(at.spec): at.packed(seqs[g][0]) for at in self.attention.values()}
             for gi, keys in enumerate(self.groups):
-                X, nm = chunk[keys[0]][0], self.normed.get(gi)
+                at = self._before.get(gi)
+                X, nm = chunk[keys[0]][0] if at is None else at.O, self.normed.get(gi)
                 if nm is not None:
                     if gi == nm.groups[0]:
                         L.lora_norm_forward(nm.desc, X, nm.X, nm.stats, stream=streams[self._on[gi]])
                     X = nm.X
                 calls[gi].forward(X, dr[gi])
+                at, q = self._after.get(gi), self._on[gi]
+                if at is not None:
+                    at.forward(packed[id(at.spec)], seqs[g][1], wss[q], streams[q])
             for gi in reversed(range(ng)):
-                keys, nm = self.groups[gi], self.normed.get(gi)
-                X = chunk[keys[0]][0] if nm is None else nm.X
-                calls[gi].backward(X, [chunk[k][1] for k in keys],
+                keys, nm, at = self.groups[gi], self.normed.get(gi), self._before.get(gi)
+                X = at.O if at is not None else chunk[keys[0]][0] if nm is None else nm.X
+                calls[gi].backward(X, [grad[k] if k in grad else chunk[k][1] for k in keys],
                                    accumulate=g > 0, drops=dr[gi])
+                if at is not None:   # wo's X is the attention's output
+                    q = self._on[gi]
+                    at.backward(packed[id(at.spec)], seqs[g][1], wss[q], streams[q])
                 if nm is not None:   # the gradients of X meet in the norm's backward
                     first, st = gi == nm.groups[-1], streams[self._on[gi]]
                     L.lora_norm_backward(nm.desc, chunk[self.groups[nm.groups[0]][0]][0],

@@ -568,16 +568,19 @@ int lora_heads_backward(int n, const lora_heads* heads, const void* const* X, co
  *
  * Q, K and V have type dtype; O, dO, dQ, dK and dV out_dtype (float32 with a
  * float32 dtype).  Scores, softmax and all sums are float32; with bf16 the
- * weights p and ds (and dO, if float32) are rounded to bf16 once, as operands
- * of their products.  Offsets and lengths are device int32 and read by the
- * kernels: offsets must not decrease, and the query rows and key rows of
- * different sequences must not overlap; what points outside the buffers is
- * cut to them.  Each tensor has ld elements between tokens and h between heads
- * (either order of the two in memory, no overlap); gradients have the strides
- * of what they are gradients of.  head_dim is a multiple of 8 up to 128, strides
- * and pointers are 16-byte aligned (LORA_E_ALIGN); heads must be a multiple of
- * kv_heads, q_tokens heads, k_tokens and seqs heads below 2^30, ldk and ldv at most 2^22
- * (LORA_E_SHAPE).  Outputs must not overlap inputs. */
+ * weights p and ds (and dO, if float32) are rounded to bf16 as operands of
+ * their products, but for dq, to whose ds a second bf16 part is added.
+ *
+ * Offsets and lengths are device int32 and read by the kernels: offsets must
+ * not decrease, and the rows of different sequences must not overlap; what
+ * points outside the buffers is cut to them.  Each tensor has ld elements
+ * between tokens and h between heads (either order of the two in memory, no
+ * overlap); gradients have the strides of what they are gradients of.
+ * head_dim is a multiple of 8 up to 128; strides and pointers are 16-byte
+ * aligned (LORA_E_ALIGN); heads is a multiple of kv_heads, q_tokens heads,
+ * k_tokens and seqs heads are below 2^30, ldk and ldv at most 2^22, and
+ * heads / kv_heads hq + 128 ldq (and the same of O) below 2^30 (LORA_E_SHAPE).
+ * Outputs must not overlap inputs. */
 typedef struct lora_attention {
   int64_t q_tokens, k_tokens;   /* rows of Q and of K and V                */
   int64_t heads, kv_heads, head_dim, seqs;
