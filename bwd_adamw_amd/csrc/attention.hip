@@ -139,7 +139,7 @@ void forward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
 // them, QT times 32 rows each a stage.
 template <typename T, int DP>
 struct BwdShape {
-  static constexpr int KW = sizeof(T) == 2 && DP == 128 ? 4 : 2, QW = 4 / KW, QT = 2 / QW, BK = 32 * KW, BQ = 64;
+  static constexpr int KW = sizeof(T) == 2 && DP == 128 ? 4 : 2, QW = 2, QT = 1, BK = 32 * KW, BQ = 32 * QW * QT;
 };
 int64_t bwd_keys(const lora_attention* a) { return a->dtype == LORA_BF16 && a->head_dim > 64 ? 128 : 64; }
 // Blocks that share a key tile's rows: enough for causal tiles, whose rows differ
@@ -192,7 +192,7 @@ void backward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
   const int64_t blocks = b.tiles * p.kv;
   {
     prof::Scope ps("attn_dkv", a->q_tokens, a->k_tokens, a->heads, 8.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 2));
-    launch_n(attn_dkv_kernel<T, OT, DP, S::KW, S::QW, S::QT>, dim3((unsigned)(blocks * b.splits)), 256u, st, ps, p);
+    launch_n(attn_dkv_kernel<T, OT, DP, S::KW, S::QW, S::QT>, dim3((unsigned)(blocks * b.splits)), 64u * S::KW * S::QW, st, ps, p);
   }
   if (b.splits > 1) {
     prof::Scope ps("attn_dkv_join", a->k_tokens, a->kv_heads, b.splits, 0.0, 8.0 * b.splits * a->kv_heads * a->k_tokens * DP);

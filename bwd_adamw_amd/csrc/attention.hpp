@@ -253,6 +253,15 @@ LORA_DEV f32x16 mma_rows(lds_char* tile, uint32_t at, const typename Frag<T>::V 
     acc = Frag<T>::mma(*(LV*)(tile + (at ^ (uint32_t)(s << 5))), f[s], acc);
   return acc;
 }
+// The same with the other operand in LDS too.
+template <typename T, int DP>
+LORA_DEV f32x16 mma_rows(lds_char* tile, uint32_t at, lds_char* other, uint32_t oat, f32x16 acc) {
+  typedef __attribute__((address_space(3))) const typename Frag<T>::V LV;
+#pragma unroll
+  for (int s = 0; s < DP / Frag<T>::FK; ++s)
+    acc = Frag<T>::mma(*(LV*)(tile + (at ^ (uint32_t)(s << 5))), *(LV*)(other + (oat ^ (uint32_t)(s << 5))), acc);
+  return acc;
+}
 // acc[dt] += (32 rows from `at`)^T x, x a product's result with the same rows
 // down its registers.  bf16: values 8 u .. 8 u + 7 of lane half h are rows
 // 16 u + 4 h + 0..3 and 16 u + 8 + 4 h + 0..3, the transpose reads' order.  TWICE
@@ -768,13 +777,15 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 ? 2 : 1) void attn_dq_
 // neighbouring tokens) with their log-sums and deltas.  p.splits blocks share a
 // key tile's stages where there are few tiles.
 template <typename T, typename OT, int DP, int KW, int QW, int QT>
-__global__ __launch_bounds__(64 * KW * QW, DP == 64 && sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(AttnArgs p) {
+__global__ __launch_bounds__(64 * KW * QW, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(AttnArgs p) {
   constexpr int NW = KW * QW, BK = 32 * KW, BQ = 32 * QW * QT, KS = DP / Frag<T>::FK, DT = DP / 32;
   constexpr bool MIXED = !std::is_same_v<T, OT>;
   typedef typename Frag<T>::V V;
   typedef Tile<T, DP, BQ, NW> Ti;
+  typedef Tile<T, DP, BK, NW> Kt;
   constexpr int SB = BQ < 64 ? 256 : 4 * BQ, STAGE = 2 * Ti::BYTES + 2 * SB;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  constexpr bool KV_LDS = sizeof(T) == 2 && DP == 128;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE + (KV_LDS ? 2 * Kt::BYTES : 0)];
   lds_char* const lds = (lds_char*)smem;
   const int split = (int)(blockIdx.x / p.kv) % p.splits;
   const KeyTile kt = attn_key_tile<true>(p, (int)(blockIdx.x / p.kv / p.splits) * p.kv + (int)(blockIdx.x % p.kv), BK);
@@ -784,9 +795,29 @@ __global__ __launch_bounds__(64 * KW * QW, DP == 64 && sizeof(T) == 2 ? 2 : 1) v
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave % KW, qw = wave / KW;
   const int key = k0 + 32 * kw + (lane & 31), kc = min(key, sq.lk - 1);
-  V kf[KS], vf[KS];
-  load_frags<T, DP>(kf, (const T*)p.K + (sq.k0 + kc) * p.ldk + kvh * p.hk, p.dim, half);
-  load_frags<T, DP>(vf, (const T*)p.V + (sq.k0 + kc) * p.ldv + kvh * p.hv, p.dim, half);
+  // bf16 at DP 128: K and V stay in LDS, which leaves the registers for two waves a
+  // SIMD (2048 tokens of 32/8 heads: 91 us); one wave with them in registers keeps
+  // the matrix cores busy for 42 % of its cycles and LDS for a quarter (104 us).
+  const T* const Kg = (const T*)p.K + (sq.k0 + k0) * p.ldk + kvh * p.hk;
+  const T* const Vg = (const T*)p.V + (sq.k0 + k0) * p.ldv + kvh * p.hv;
+  lds_char* const Kl = lds + 2 * STAGE;
+  lds_char* const Vl = Kl + Kt::BYTES;
+  const uint32_t kat = rows_at<T, DP>(32 * kw, lane);
+  V kf[KV_LDS ? 1 : KS], vf[KV_LDS ? 1 : KS];
+  if constexpr (KV_LDS) {
+    const int64_t left = sq.lk - k0 - 1;
+    const u32x4 rk = attn_rsrc(Kg, (left * p.ldk + p.dim) * (int)sizeof(T));
+    const u32x4 rv = attn_rsrc(Vg, (left * p.ldv + p.dim) * (int)sizeof(T));
+#pragma unroll
+    for (int q = 0; q < Kt::PER; ++q) {
+      const int r = Kt::row(wave, q, lane), d = Kt::chunk(wave, q, lane) * Frag<T>::E;
+      load_lds16(rk, Kl + 1024 * (wave * Kt::PER + q), d < p.dim ? (uint32_t)((r * p.ldk + d) * (int)sizeof(T)) : kNowhere);
+      load_lds16(rv, Vl + 1024 * (wave * Kt::PER + q), d < p.dim ? (uint32_t)((r * p.ldv + d) * (int)sizeof(T)) : kNowhere);
+    }
+  } else {
+    load_frags<T, DP>(kf, Kg + (kc - k0) * p.ldk, p.dim, half);
+    load_frags<T, DP>(vf, Vg + (kc - k0) * p.ldv, p.dim, half);
+  }
   f32x16 dk[DT] = {}, dv[DT] = {};
   // The first row that sees key j is sees(j): causal row m sees up to m / G + lk - lq.
   auto sees = [&](int j) { return p.causal ? max(j - (sq.lk - sq.lq), 0) * p.group : 0; };
@@ -856,8 +887,14 @@ __global__ __launch_bounds__(64 * KW * QW, DP == 64 && sizeof(T) == 2 ? 2 : 1) v
 #pragma unroll
         for (int e = 0; e < 4; ++e) ds[4 * q + e] = de[e];
       }
-      f32x16 s = mma_rows<T, DP>(Qs + 32 * j * Ti::ROWB, rat, kf);
-      ds = mma_rows<T, DP>(Ds + 32 * j * Ti::ROWB, rat, vf, ds);
+      f32x16 s = {};
+      if constexpr (KV_LDS) {
+        s = mma_rows<T, DP>(Qs + 32 * j * Ti::ROWB, rat, Kl, kat, s);
+        ds = mma_rows<T, DP>(Ds + 32 * j * Ti::ROWB, rat, Vl, kat, ds);
+      } else {
+        s = mma_rows<T, DP>(Qs + 32 * j * Ti::ROWB, rat, kf, s);
+        ds = mma_rows<T, DP>(Ds + 32 * j * Ti::ROWB, rat, vf, ds);
+      }
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
         s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], p.c, -ls[v >> 2][v & 3]));
