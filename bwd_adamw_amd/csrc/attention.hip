@@ -86,23 +86,28 @@ double attn_bytes(const lora_attention* a, int n) {
   return a->head_dim * (a->q_tokens * a->heads * (e + n * oe) + a->k_tokens * a->kv_heads * (2 * e + (n > 1 ? 2 * oe : 0)));
 }
 
-// The forward's kernel: 128 rows a block, or 32 rows with the keys of a stage
-// dealt to its waves where a sequence has no more; and the blocks that share a
-// row tile's keys, so that few rows still fill the chip, with 256 keys each at
-// least (by the sequences' mean room: lengths are known to the kernels only).
+// The forward's kernel: four waves of 32 rows a block; two, times two that share
+// a stage's keys, where four would leave CUs idle; one where a sequence has no
+// more than 32 rows (single tokens: blocks of their own, which load and compute at
+// different times, read cold caches of 32 requests up to 4096 keys at 4.2 TB/s,
+// four waves in step at 3.8).  Then the blocks that share a row tile's keys, so
+// that few rows still fill the chip: 128 keys each at least for single tokens,
+// else 256 (by the sequences' mean room: lengths are known to the kernels only).
 struct FwdPlan {
-  int rw;                  // waves of 32 rows: 1 or 2 (times waves that share a stage's keys) or 4
+  int rw;                  // waves of 32 rows
   int64_t tiles, splits;
 };
 FwdPlan fwd_plan(const lora_attention* a) {
-  const int64_t group = a->heads / a->kv_heads;
+  const int64_t group = a->heads / a->kv_heads, room = a->k_tokens / a->seqs;
   FwdPlan f;
   f.rw = a->q_tokens * group <= 32 * a->seqs                                     ? 1
          : tile_count(a->q_tokens, group, a->seqs, 128) * a->kv_heads < kCUs ? 2
                                                                              : 4;
   f.tiles = tile_count(a->q_tokens, group, a->seqs, 32 * f.rw);
-  f.splits = clampi(cdiv(4 * kCUs, f.tiles * a->kv_heads), 1, clampi(a->k_tokens / a->seqs / 256, 1, 64));
-  if (f.rw > 1 && f.tiles * a->kv_heads >= kCUs) f.splits = 1;
+  const int64_t blocks = f.tiles * a->kv_heads;
+  f.splits = f.rw == 1 ? clampi(cdiv(8 * kCUs, blocks), 1, clampi(room / 128, 1, 64))
+             : blocks < kCUs ? clampi(cdiv(4 * kCUs, blocks), 1, clampi(room / 256, 1, 64))
+                             : 1;
   return f;
 }
 // Bytes of the splits' sums, and of their maxima and weights behind them.
@@ -130,7 +135,7 @@ void forward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
   p.splits = (int32_t)f.splits;
   p.part = (float*)ws;
   p.ml = (float*)((char*)ws + part_bytes(a, f, false));
-  if (f.rw == 1) forward_by<T, OT, DP, 1, sizeof(T) == 2 ? 4 : 2, 1>(a, p, st);
+  if (f.rw == 1) forward_by<T, OT, DP, 1, 1, 1>(a, p, st);
   else if (f.rw == 2) forward_by<T, OT, DP, 2, 2, 1>(a, p, st);
   else forward_by<T, OT, DP, 4, 1, sizeof(T) == 2 ? 2 : 1>(a, p, st);
 }

@@ -404,10 +404,10 @@ LORA_DEV RowTile attn_row_tile(const AttnArgs& p, int b, int BM) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  A block has RW waves of 32 rows, times CW that share a stage's keys
-// (few rows: single tokens over a cache).  A stage is BN keys of K and V in
-// LDS; the next one loads while one is used.  p.splits blocks share a row
-// tile's stages where there are few tiles, and attn_join_kernel adds them up.
+// Forward.  A block has RW waves of 32 rows, times CW that share a stage's keys.  A
+// stage is BN keys of K and V in LDS; the next one loads while one is used.
+// p.splits blocks share a row tile's stages where there are few tiles (single
+// tokens over caches), and attn_join_kernel adds them up.
 //
 // The running maximum is only raised where it grew by more than 8 (in powers of
 // two): the weights then stay under 2^8 and nothing is lost, and most stages
@@ -476,7 +476,7 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 && CW == 1 ? 2 : 1) vo
 #pragma unroll
       for (int j = 0; j < KT; ++j)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) s[j][v] = kb + 32 * j + row32(v, lane) >= lim ? -INFINITY : s[j][v];
+        for (int v = 0; v < 16; ++v) s[j][v] = 32 * j + row32(v, 0) >= lim - kb - 4 * half ? -INFINITY : s[j][v];
     }
 #pragma unroll
     for (int j = 0; j < KT; ++j)
@@ -756,7 +756,7 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 ? 2 : 1) void attn_dq_
       for (int v = 0; v < 16; ++v) s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], p.c, -lse2)) * dp[v];
       if (kb + 32 * j + 32 > least) {   // after the products: what a masked score gives must not count
 #pragma unroll
-        for (int v = 0; v < 16; ++v) s[v] = kb + 32 * j + row32(v, lane) >= lim ? 0.0f : s[v];
+        for (int v = 0; v < 16; ++v) s[v] = 32 * j + row32(v, 0) >= lim - kb - 4 * half ? 0.0f : s[v];
       }
       mma_cols<T, DP, true>(dq, Ks + 32 * j * Ti::ROWB, cat, s);
     }
@@ -903,7 +903,7 @@ __global__ __launch_bounds__(64 * KW * QW, sizeof(T) == 2 ? 2 : 1) void attn_dkv
       if (mb < all) {
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-          const bool in = mb + row32(v, lane) >= mine;
+          const bool in = row32(v, 0) >= mine - mb - 4 * half;
           s[v] = in ? s[v] : 0.0f;
           ds[v] = in ? ds[v] : 0.0f;
         }

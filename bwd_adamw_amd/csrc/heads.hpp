@@ -281,11 +281,21 @@ __global__ __launch_bounds__(1024) void heads_finish_kernel(HeadsArgs p, int par
   if (!d.dgamma) return;
   const int cx = threadIdx.x & 31, py = threadIdx.x >> 5, c = blockIdx.x * 32 + cx;
   double s = 0.0;
-  if (c < d.dim)
-    for (int i = py; i < parts; i += 32) s += (double)d.part[(int64_t)i * d.dim + c];
+  if (c < d.dim) {
+    // Sixteen loads at a time (past the last partial it is read again and not
+    // added): 512 partials are one round trip, 6.1 -> 3.4 us.
+    for (int i = py; i < parts; i += 16 * 32) {
+      float v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = d.part[(int64_t)min(i + 32 * k, parts - 1) * d.dim + c];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s += i + 32 * k < parts ? (double)v[k] : 0.0;
+    }
+  }
   red[py][cx] = s;
   __syncthreads();
   if (py == 0 && c < d.dim) {
+#pragma unroll
     for (int i = 1; i < 32; ++i) s += red[i][cx];
     d.dgamma[c] = (float)(p.accumulate ? (double)d.dgamma[c] + s : s);
   }
