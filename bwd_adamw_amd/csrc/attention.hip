@@ -43,7 +43,7 @@ int check_attn(const lora_attention* a) {
     return LORA_E_SHAPE;
   // Rows of a tile are addressed with 32-bit byte offsets from its first token.
   const int64_t group = a->heads / a->kv_heads;
-  if (group * a->hq + 128 * a->ldq >= kMaxRows / 2 || group * a->ho + 128 * a->ldo >= kMaxRows / 2) return LORA_E_SHAPE;
+  if (group * a->hq + 128 * a->ldq >= kMaxRows / 4 || group * a->ho + 128 * a->ldo >= kMaxRows / 4) return LORA_E_SHAPE;
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale) || !a->q_offsets || !a->k_offsets) return LORA_E_INVALID;
   const int64_t e = elem(a->dtype), oe = elem(a->out_dtype);
   if (a->head_dim % 8 || !al_to(a->ldq, e) || !al_to(a->hq, e) || !al_to(a->ldk, e) || !al_to(a->hk, e) ||

@@ -579,7 +579,7 @@ int lora_heads_backward(int n, const lora_heads* heads, const void* const* X, co
  * head_dim is a multiple of 8 up to 128; strides and pointers are 16-byte
  * aligned (LORA_E_ALIGN); heads is a multiple of kv_heads, q_tokens heads,
  * k_tokens and seqs heads are below 2^30, ldk and ldv at most 2^22, and
- * heads / kv_heads hq + 128 ldq (and the same of O) below 2^30 (LORA_E_SHAPE).
+ * heads / kv_heads hq + 128 ldq (and the same of O) below 2^29 (LORA_E_SHAPE).
  * Outputs must not overlap inputs. */
 typedef struct lora_attention {
   int64_t q_tokens, k_tokens;   /* rows of Q and of K and V                */
