@@ -926,6 +926,29 @@ def _device_ints(t, name, need):
     return _sized(t, name, need, torch.int32)
 
 
+def _here(stream):
+    """The current device, on which a call's kernels are launched (-2: none;
+    -1 is what CPU tensors are on)."""
+    try:
+        here = torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != here:
+        raise ValueError(f"the stream is of GPU {stream.device_index}, the current one is {here}")
+    return here
+
+
+def _stream_on(stream, here):
+    """_stream, with the current device known."""
+    return _raw_stream(here) if stream is None and _raw_stream is not None and here >= 0 else _stream(stream)
+
+
+def _all_here(here, *ts):
+    for t in ts:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor of the call is on GPU {t.get_device()}, the current one is {here}")
+
+
 def make_heads(tokens, heads, head_dim, x_dtype=torch.float32, y_dtype=None, norm=True, eps=1e-6, gamma=None,
                rot_dim=None, freqs=None, interleaved=False, ldx=None, hx=None, ldy=None,
                hy=None) -> LoraHeads:
@@ -946,10 +969,10 @@ def make_heads(tokens, heads, head_dim, x_dtype=torch.float32, y_dtype=None, nor
     return out
 
 
-def _strided(t, name, i, tokens, heads, dim, ld, h, dtype):
-    """Device pointer of heads whose tokens are ld and heads h elements apart:
-    a [tokens, heads, dim] tensor of those strides, or (where the heads of a
-    token lie together) [tokens, heads * dim]."""
+def _strided(t, name, i, tokens, heads, dim, ld, h, dtype, here):
+    """Device pointer, on GPU `here`, of heads whose tokens are ld and heads h
+    elements apart: a [tokens, heads, dim] tensor of those strides, or (where
+    the heads of a token lie together) [tokens, heads * dim]."""
     if t is None:
         return None
     name = name if i is None else f"{name}[{i}]"
@@ -957,6 +980,7 @@ def _strided(t, name, i, tokens, heads, dim, ld, h, dtype):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
+    _all_here(here, t)
     if _act(t.dtype) != dtype:
         raise TypeError(f"{name} must be {'float32' if dtype == F32 else 'bfloat16'}, got {t.dtype}")
     if t.dim() == 2 and tuple(t.shape) == (tokens, heads * dim) and (h == dim or heads == 1):
@@ -970,18 +994,18 @@ def _strided(t, name, i, tokens, heads, dim, ld, h, dtype):
     return t.data_ptr()
 
 
-def _head_ptr(t, name, i, tokens, heads, dim, ld, h, dtype):
+def _head_ptr(t, name, i, tokens, heads, dim, ld, h, dtype, here):
     """_strided, in few steps for the usual tensors (a token's call is host
     time: the checks above take 2 us a tensor)."""
-    if type(t) is torch.Tensor and t.is_cuda and _ACT_DTYPES.get(t.dtype) == dtype:
+    if type(t) is torch.Tensor and t.get_device() == here and _ACT_DTYPES.get(t.dtype) == dtype:
         shape, st = t.shape, t.stride()
         if (shape == (tokens, heads, dim) and st == (ld, h, 1)) or \
                 (h == dim and shape == (tokens, heads * dim) and st == (ld, 1)):
             return t.data_ptr()
-    return _strided(t, name, i, tokens, heads, dim, ld, h, dtype)
+    return _strided(t, name, i, tokens, heads, dim, ld, h, dtype, here)
 
 
-def _head_ptrs(heads, ts, name, x):
+def _head_ptrs(heads, ts, name, x, here):
     if ts is None:
         return None
     if len(ts) != len(heads):
@@ -989,7 +1013,7 @@ def _head_ptrs(heads, ts, name, x):
     out = (C.c_void_p * len(ts))()
     for i, d in enumerate(heads):
         out[i] = _head_ptr(ts[i], name, i, d.tokens, d.heads, d.head_dim,
-                           *((d.ldx, d.hx, d.x_dtype) if x else (d.ldy, d.hy, d.y_dtype)))
+                           *((d.ldx, d.hx, d.x_dtype) if x else (d.ldy, d.hy, d.y_dtype)), here)
     return out
 
 
@@ -997,9 +1021,11 @@ def lora_heads_forward(heads, X, Y, positions=None, stream=None):
     """Y[i] = the heads X[i], normed and rotated, for each set of `heads` (one
     to four of the same tokens); positions [tokens] int32."""
     arr = (LoraHeads * len(heads))(*heads)
-    rc = lib().lora_heads_forward(len(heads), arr, _head_ptrs(heads, X, "X", True), _head_ptrs(heads, Y, "Y", False),
-                                  _device_ints(positions, "positions", heads[0].tokens if len(heads) else 0),
-                                  _stream(stream))
+    here = _here(stream)
+    px, py = _head_ptrs(heads, X, "X", True, here), _head_ptrs(heads, Y, "Y", False, here)
+    pos = _device_ints(positions, "positions", heads[0].tokens if len(heads) else 0)
+    _all_here(here, positions, *[t for d in heads for t in getattr(d, "vectors", ())])
+    rc = lib().lora_heads_forward(len(heads), arr, px, py, pos, _stream_on(stream, here))
     _check("lora_heads_forward", rc)
 
 
@@ -1017,15 +1043,17 @@ def lora_heads_backward(heads, X, dY, dX=None, dgamma=None, positions=None, accu
         raise ValueError(f"dgamma has {len(dgamma)} entries for {len(heads)} sets of heads")
     dg = None if dgamma is None else (C.c_void_p * len(heads))(
         *[_sized(t, f"dgamma[{i}]", h.head_dim) for i, (t, h) in enumerate(zip(dgamma, heads))])
+    here = _here(stream)
+    px, py = _head_ptrs(heads, X, "X", True, here), _head_ptrs(heads, dY, "dY", False, here)
+    pdx = _head_ptrs(heads, dX, "dX", True, here)
+    pos = _device_ints(positions, "positions", heads[0].tokens if len(heads) else 0)
+    _all_here(here, positions, ws, *(dgamma or ()), *[t for d in heads for t in getattr(d, "vectors", ())])
     if ws is None and dgamma is not None and any(t is not None for t in dgamma):
         need = int(lib().lora_heads_workspace_bytes(len(heads), arr))
         if need:
             ws = _own_ws(need, dY[0].device, stream)
-    rc = lib().lora_heads_backward(len(heads), arr, _head_ptrs(heads, X, "X", True), _head_ptrs(heads, dY, "dY", False),
-                                   _head_ptrs(heads, dX, "dX", True), dg,
-                                   _device_ints(positions, "positions", heads[0].tokens if len(heads) else 0),
-                                   1 if accumulate else 0, _ptr(ws, "ws", None),
-                                   0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    rc = lib().lora_heads_backward(len(heads), arr, px, py, pdx, dg, pos, 1 if accumulate else 0, _ptr(ws, "ws", None),
+                                   0 if ws is None else ws.numel() * ws.element_size(), _stream_on(stream, here))
     _check("lora_heads_backward", rc)
 
 
@@ -1053,40 +1081,44 @@ def lora_attention_workspace_bytes(at: LoraAttention, backward=False) -> int:
     return int(lib().lora_attention_workspace_bytes(C.byref(at), 1 if backward else 0))
 
 
-def _attn_ptrs(at, ts):
+def _attn_ptrs(at, ts, here):
     """Device pointers of tensors laid out like Q, K, V or O: (tensor, name,
     whose strides, whether of out_dtype)."""
     q, k, d, io = (at.q_tokens, at.heads), (at.k_tokens, at.kv_heads), at.head_dim, (at.dtype, at.out_dtype)
     lay = {"q": (*q, d, at.ldq, at.hq), "k": (*k, d, at.ldk, at.hk), "v": (*k, d, at.ldv, at.hv),
            "o": (*q, d, at.ldo, at.ho)}
-    return [_head_ptr(t, name, None, *lay[of], io[out]) for t, name, of, out in ts]
+    return [_head_ptr(t, name, None, *lay[of], io[out], here) for t, name, of, out in ts]
 
 
 def lora_attention_forward(at: LoraAttention, Q, K, V, O, lse=None, ws=None, stream=None):
     """O = attention of Q over K and V; lse [heads, q_tokens] float32 receives
     what the backward needs.  `ws` is taken from torch's allocator when one is
     needed and it is None."""
-    ptrs = _attn_ptrs(at, ((Q, "Q", "q", 0), (K, "K", "k", 0), (V, "V", "v", 0), (O, "O", "o", 1)))
+    here = _here(stream)
+    ptrs = _attn_ptrs(at, ((Q, "Q", "q", 0), (K, "K", "k", 0), (V, "V", "v", 0), (O, "O", "o", 1)), here)
     ptrs.append(_sized(lse, "lse", at.heads * at.q_tokens))
+    _all_here(here, lse, ws, *getattr(at, "vectors", ()))
     if ws is None:
         need = int(lib().lora_attention_workspace_bytes(C.byref(at), 0))
         if need:
             ws = _own_ws(need, O.device, stream)
     rc = lib().lora_attention_forward(C.byref(at), *ptrs, _ptr(ws, "ws", None),
-                                      0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+                                      0 if ws is None else ws.numel() * ws.element_size(), _stream_on(stream, here))
     _check("lora_attention_forward", rc)
 
 
 def lora_attention_backward(at: LoraAttention, Q, K, V, O, dO, lse, dQ, dK, dV, ws=None, stream=None):
     """Gradients of lora_attention_forward from dO; `ws` is taken from torch's
     allocator when None."""
+    here = _here(stream)
     ptrs = _attn_ptrs(at, ((Q, "Q", "q", 0), (K, "K", "k", 0), (V, "V", "v", 0), (O, "O", "o", 1), (dO, "dO", "o", 1),
-                           (dQ, "dQ", "q", 1), (dK, "dK", "k", 1), (dV, "dV", "v", 1)))
+                           (dQ, "dQ", "q", 1), (dK, "dK", "k", 1), (dV, "dV", "v", 1)), here)
     ptrs.insert(5, _sized(lse, "lse", at.heads * at.q_tokens))
+    _all_here(here, lse, ws, *getattr(at, "vectors", ()))
     if ws is None:
         ws = _own_ws(max(16, int(lib().lora_attention_workspace_bytes(C.byref(at), 1))), dQ.device, stream)
     rc = lib().lora_attention_backward(C.byref(at), *ptrs, _ptr(ws, "ws", None), ws.numel() * ws.element_size(),
-                                       _stream(stream))
+                                       _stream_on(stream, here))
     _check("lora_attention_backward", rc)
 
 

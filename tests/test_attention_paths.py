@@ -152,3 +152,27 @@ def test_heads_then_attention_and_back():
     for got, ref in [(o, orf)] + list(zip(dy, [y.grad for y in yr])) + list(zip(dg, [x.grad for x in gr])):
         ref = ref.detach()
         assert (got.cpu().double() - ref).abs().max() <= 16 * HALF * ref.abs().max()
+
+
+@pytest.mark.gpu
+def test_calls_on_another_device_than_the_current_one_are_refused(monkeypatch):
+    """Kernels are launched on the current device: tensors (and streams) of
+    another are refused before anything is."""
+    bf = torch.bfloat16
+    x = torch.randn(4, 2, 64, device="cuda", dtype=bf)
+    off = torch.tensor([0, 4], device="cuda", dtype=torch.int32)
+    heads = [L.make_heads(4, 2, 64, bf, bf)]
+    at = L.make_attention(4, 4, 2, 2, 64, off, off)
+    y, lse, stream = torch.full_like(x, 7.0), torch.zeros(2, 4, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for s in (None, stream):
+        for call in (lambda: L.lora_heads_forward(heads, [x], [y], stream=s),
+                     lambda: L.lora_heads_backward(heads, [x], [x], [y], stream=s),
+                     lambda: L.lora_attention_forward(at, x, x, x, y, stream=s),
+                     lambda: L.lora_attention_backward(at, x, x, x, x, x, lse, y, y, y, stream=s)):
+            with pytest.raises(ValueError, match="GPU 0, the current one is 1"):
+                call()
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert (y == 7.0).all()
