@@ -174,7 +174,7 @@ BwdSpace bwd_space(const lora_attention* a) {
   BwdSpace w;
   w.dO16 = (size_t)rup(2 * rows * 4, 256);
   w.part = w.dO16 + (a->dtype != a->out_dtype ? (size_t)rup(rows * dp * 2, 256) : 0);
-  w.total = w.part + (b.splits > 1 ? (size_t)(b.splits * a->kv_heads * a->k_tokens * 2 * dp * 4) : 0);
+  w.total = w.part + (b.splits > 1 ? (size_t)(b.splits * a->kv_heads * b.tiles * bwd_keys(a) * 2 * dp * 4) : 0);
   return w;
 }
 
@@ -207,7 +207,7 @@ void backward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
   }
   if (b.splits > 1) {
     prof::Scope ps("attn_dkv_join", a->k_tokens, a->kv_heads, b.splits, 0.0, 8.0 * b.splits * a->kv_heads * a->k_tokens * DP);
-    launch_n(attn_dkv_join_kernel<OT, DP, S::BK>, dim3((unsigned)blocks, S::BK * DP / 512), 256u, st, ps, p);
+    launch_n(attn_dkv_join_kernel<OT, DP, S::BK>, dim3((unsigned)blocks, S::BK * DP / 512 / 2), 256u, st, ps, p);
   }
 }
 

@@ -137,6 +137,21 @@ LORA_DEV typename Frag<T>::V frag_of(const OT* g) {
     return u32x4{cvt_bf16x2(a[0], a[1]), cvt_bf16x2(a[2], a[3]), cvt_bf16x2(b[0], b[1]), cvt_bf16x2(b[2], b[3])};
   }
 }
+// What a lane's fragments of two rows add to their product.
+template <typename T>
+LORA_DEV float dot_frags(const typename Frag<T>::V& a, const typename Frag<T>::V& b) {
+  float x = 0.0f;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x += a[e] * b[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x += __uint_as_float(a[e] << 16) * __uint_as_float(b[e] << 16) +
+           __uint_as_float(a[e] & 0xffff0000u) * __uint_as_float(b[e] & 0xffff0000u);
+  }
+  return x;
+}
 // A row's register operand: fragment s holds values FK s + E half ...
 template <typename T, int DP, typename OT>
 LORA_DEV void load_frags(typename Frag<T>::V (&f)[DP / Frag<T>::FK], const OT* row, int dim, int half) {
@@ -153,17 +168,33 @@ LORA_DEV void store_4(OT* g, float a, float b, float c, float d) {
   if constexpr (sizeof(OT) == 4) *reinterpret_cast<f32x4*>(g) = f32x4{a, b, c, d};
   else *reinterpret_cast<u32x2*>(g) = u32x2{cvt_bf16x2(a, b), cvt_bf16x2(c, d)};
 }
-// acc^T [d][row] times f to the row at g.
+// Values d + 4 half .. (a) and d + 8 + 4 half .. (b) of a product's row, times f, to
+// the row at g, if `ok` (both per lane).  bf16: the two halves swap, so that each
+// stores 16 bytes (20 sequences of 200, 32/8 heads of 128: forward 30 -> 26 us).
+template <typename OT>
+LORA_DEV void store_pair(OT* g, bool ok, int d, f32x4 a, f32x4 b, float f, int dim, int half) {
+  a *= f, b *= f;
+  if constexpr (sizeof(OT) == 2) {
+    const auto x = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(a[0], a[1]), cvt_bf16x2(b[0], b[1]), false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(a[2], a[3]), cvt_bf16x2(b[2], b[3]), false, false);
+    if (ok && d + 8 * half < dim) *reinterpret_cast<u32x4*>(g + d + 8 * half) = u32x4{x[0], y[0], x[1], y[1]};
+  } else {
+    if (ok && d + 4 * half < dim) *reinterpret_cast<f32x4*>(g + d + 4 * half) = a;
+    if (ok && d + 8 + 4 * half < dim) *reinterpret_cast<f32x4*>(g + d + 8 + 4 * half) = b;
+  }
+}
+// acc^T [d][row] times f to the row at g, if `ok`.
 template <int DP, typename OT, int CW = 1>
-LORA_DEV void store_row(OT* g, const f32x16 (&acc)[DP / 32], float f, int dim, int half, int cw = 0) {
+LORA_DEV void store_row(OT* g, bool ok, const f32x16 (&acc)[DP / 32], float f, int dim, int half, int cw = 0) {
 #pragma unroll
-  for (int dt = 0; dt < DP / 32; ++dt)
+  for (int dt = 0; dt < DP / 32; ++dt) {
+    if (dt % CW != cw) continue;
+    const f32x16& a = acc[dt];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int d = 32 * dt + 8 * q + 4 * half;
-      if (d < dim && dt % CW == cw)
-        store_4(g + d, acc[dt][4 * q] * f, acc[dt][4 * q + 1] * f, acc[dt][4 * q + 2] * f, acc[dt][4 * q + 3] * f);
-    }
+    for (int v = 0; v < 16; v += 8)
+      store_pair(g, ok, 32 * dt + 2 * v, f32x4{a[v], a[v + 1], a[v + 2], a[v + 3]},
+                 f32x4{a[v + 4], a[v + 5], a[v + 6], a[v + 7]}, f, dim, half);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -558,15 +589,15 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 && CW == 1 ? 2 : 1) vo
       }
     }
   }
-  if (m >= rows) return;
+  const bool ok = m < rows;
   if (p.splits > 1) {
     const int64_t at = ((int64_t)split * p.kv + kvh) * (p.q_tokens * p.group) + (int64_t)sq.q0 * p.group + m;
-    store_row<DP, float, CW>(p.part + at * DP, o, 1.0f, DP, half, cw);
-    if (cw == 0 && half == 0) *reinterpret_cast<f32x2*>(p.ml + 2 * at) = f32x2{m2, l};
+    store_row<DP, float, CW>(p.part + at * DP, ok, o, 1.0f, DP, half, cw);
+    if (ok && cw == 0 && half == 0) *reinterpret_cast<f32x2*>(p.ml + 2 * at) = f32x2{m2, l};
     return;
   }
-  store_row<DP, OT, CW>((OT*)p.O + (sq.q0 + tok) * p.ldo + head * p.ho, o, l == 0.0f ? 0.0f : 1.0f / l, p.dim, half, cw);
-  if (p.lse && cw == 0 && half == 0)
+  store_row<DP, OT, CW>((OT*)p.O + (sq.q0 + tok) * p.ldo + head * p.ho, ok, o, l == 0.0f ? 0.0f : 1.0f / l, p.dim, half, cw);
+  if (ok && p.lse && cw == 0 && half == 0)
     p.lse[head * p.q_tokens + sq.q0 + tok] = l == 0.0f ? -INFINITY : (m2 + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
@@ -648,7 +679,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
 // The block's sequence and key tile.
 struct KeyTile {
   AttnSeq s;
-  int k0, kvh;
+  int k0, kvh, slot;   // first key, key head, place among all tiles
 };
 template <bool RANKED>
 LORA_DEV KeyTile attn_key_tile(const AttnArgs& p, int b, int BK) {
@@ -661,12 +692,21 @@ LORA_DEV KeyTile attn_key_tile(const AttnArgs& p, int b, int BK) {
     const Ranked k = attn_ranked(b / p.kv, (s.lk + BK - 1) / BK, s.lk / BK, p.seqs);
     r.s = uniform_seq(s, k.lane);
     r.k0 = k.place < 0 ? -1 : k.place * BK;
+    r.slot = r.s.k0 / BK + k.lane + k.place;
   } else {
     const int t = b / p.kv, i = attn_find(p.ko, p.seqs, p.k_tokens, 1, BK, t);
     r.s = uniform_seq(attn_seq(p, i), 0);
     r.k0 = __builtin_amdgcn_readfirstlane((t - attn_first(p.ko, p.k_tokens, 1, BK, i)) * BK);
+    r.slot = t;
   }
   return r;
+}
+
+// A split's sums of a key tile: of each 32 keys dK's, then dV's, in a product's layout
+// (64 lanes times 16 bytes a store).
+template <int DP>
+LORA_DEV f32x4* attn_part(const AttnArgs& p, int split, const KeyTile& k, int BK) {
+  return reinterpret_cast<f32x4*>(p.part) + (((int64_t)split * p.kv + k.kvh) * p.tiles + k.slot) * (BK * 2 * DP / 4);
 }
 
 // Wave (a, 0)'s acc += those of waves (a, 1 .. B - 1), in that order, over LDS.
@@ -716,34 +756,6 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 ? 2 : 1) void attn_dq_
   const int most = attn_limit(p, sq, (min(m0 + BM, rows) - 1) / p.group);
   const int least = attn_limit(p, sq, min(m0 + 32 * rw, rows - 1) / p.group);
   V qf[KS], df[KS];
-  load_frags<T, DP>(qf, (const T*)p.Q + (sq.q0 + tok) * p.ldq + head * p.hq, p.dim, half);
-  const OT* dor = (const OT*)p.dO + (sq.q0 + tok) * p.ldo + head * p.ho;
-  const OT* orow = (const OT*)p.O + (sq.q0 + tok) * p.ldo + head * p.ho;
-  load_frags<T, DP>(df, dor, p.dim, half);
-  float delta = 0.0f;
-#pragma unroll
-  for (int k = 0; k < DP / 8; ++k) {
-    const int d = 8 * k + 4 * half;
-    if (d >= p.dim) continue;
-    const f32x4 a = load4(dor + d), b = load4(orow + d);
-    delta += (a[0] * b[0] + a[1] * b[1]) + (a[2] * b[2] + a[3] * b[3]);
-  }
-  delta += other_half(delta);
-  const float lse = p.lse[head * p.q_tokens + sq.q0 + tok];
-  const float lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;   // (no keys: nothing below counts)
-  const int64_t R = p.q_tokens * p.group, at = kvh * R + (int64_t)sq.q0 * p.group + m;
-  if (cw == 0 && m < rows) {   // for the pass over key tiles
-    if (half == 0) {
-      p.stat[at] = lse2;
-      p.stat[p.kv * R + at] = -delta;
-    }
-    if constexpr (MIXED) {
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-        *reinterpret_cast<V*>((T*)p.dO16 + at * DP + Frag<T>::FK * s + Frag<T>::E * half) = df[s];
-    }
-  }
-  f32x16 dq[DT] = {};
   const T* Kg = (const T*)p.K + sq.k0 * p.ldk + kvh * p.hk;
   const T* Vg = (const T*)p.V + sq.k0 * p.ldv + kvh * p.hv;
   uint32_t ka[Ti::PER], va[Ti::PER];
@@ -762,6 +774,42 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 ? 2 : 1) void attn_dq_
     Ti::load(attn_rsrc(vp, vleft), lds + buf * STAGE + Ti::BYTES, wave, va);
     kp += kstep, vp += vstep, kleft -= kstep, vleft -= vstep;
   };
+  if (most > 0) load(0);
+  load_frags<T, DP>(qf, (const T*)p.Q + (sq.q0 + tok) * p.ldq + head * p.hq, p.dim, half);
+  const OT* dor = (const OT*)p.dO + (sq.q0 + tok) * p.ldo + head * p.ho;
+  const OT* orow = (const OT*)p.O + (sq.q0 + tok) * p.ldo + head * p.ho;
+  load_frags<T, DP>(df, dor, p.dim, half);
+  float delta = 0.0f;
+  if constexpr (MIXED) {
+#pragma unroll
+    for (int k = 0; k < DP / 8; ++k) {
+      const int d = 8 * k + 4 * half;
+      if (d >= p.dim) continue;
+      const f32x4 a = load4(dor + d), b = load4(orow + d);
+      delta += (a[0] * b[0] + a[1] * b[1]) + (a[2] * b[2] + a[3] * b[3]);
+    }
+  } else {
+    V of[KS];
+    load_frags<T, DP>(of, orow, p.dim, half);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) delta += dot_frags<T>(df[s], of[s]);
+  }
+  delta += other_half(delta);
+  const float lse = p.lse[head * p.q_tokens + sq.q0 + tok];
+  const float lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;   // (no keys: nothing below counts)
+  const int64_t R = p.q_tokens * p.group, at = kvh * R + (int64_t)sq.q0 * p.group + m;
+  if (cw == 0 && m < rows) {   // for the pass over key tiles
+    if (half == 0) {
+      p.stat[at] = lse2;
+      p.stat[p.kv * R + at] = -delta;
+    }
+    if constexpr (MIXED) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        *reinterpret_cast<V*>((T*)p.dO16 + at * DP + Frag<T>::FK * s + Frag<T>::E * half) = df[s];
+    }
+  }
+  f32x16 dq[DT] = {};
   const uint32_t rat = rows_at<T, DP>(32 * KT * cw, lane), cat = cols_at<T, DP>(32 * KT * cw, lane);
   auto step = [&](int k0, auto B) {
     constexpr int buf = decltype(B)::value;
@@ -786,15 +834,13 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 ? 2 : 1) void attn_dq_
       mma_cols<T, DP, true>(dq, Ks + 32 * j * Ti::ROWB, cat, s);
     }
   };
-  if (most > 0) load(0);
   wait_loads();
   for (int kb = 0; kb < most; kb += 2 * BN) {
     step(kb, std::integral_constant<int, 0>{});
     if (kb + BN < most) step(kb + BN, std::integral_constant<int, 1>{});
   }
   if constexpr (CW > 1) add_waves<DP, RW, CW, 2 * STAGE>(dq, smem, rw, cw, lane);
-  if (cw > 0 || m >= rows) return;
-  store_row<DP>((OT*)p.dQ + (sq.q0 + tok) * p.ldq + head * p.hq, dq, p.scale, p.dim, half);
+  if (cw == 0) store_row<DP>((OT*)p.dQ + (sq.q0 + tok) * p.ldq + head * p.hq, m < rows, dq, p.scale, p.dim, half);
 }
 
 // dK and dV.  A block's KW waves have 32 keys each, times QW that share a stage's
@@ -945,38 +991,52 @@ __global__ __launch_bounds__(64 * KW * QW, sizeof(T) == 2 ? 2 : 1) void attn_dkv
     step(st, std::integral_constant<int, 0>{});
     if (st + 1 < st1) step(st + 1, std::integral_constant<int, 1>{});
   }
-  if constexpr (QW > 1) {
-    add_waves<DP, KW, QW, 2 * STAGE>(dk, smem, kw, qw, lane);
-    add_waves<DP, KW, QW, 2 * STAGE>(dv, smem, kw, qw, lane);
-    if (qw > 0) return;
-  }
-  if (key >= sq.lk) return;
-  if (p.splits > 1) {
-    float* g = p.part + (((int64_t)split * p.kv + kvh) * p.k_tokens + sq.k0 + key) * 2 * DP;
-    store_row<DP>(g, dk, 1.0f, DP, half);
-    store_row<DP>(g + DP, dv, 1.0f, DP, half);
-    return;
-  }
-  store_row<DP>((OT*)p.dK + (sq.k0 + key) * p.ldk + kvh * p.hk, dk, p.scale, p.dim, half);
-  store_row<DP>((OT*)p.dV + (sq.k0 + key) * p.ldv + kvh * p.hv, dv, 1.0f, p.dim, half);
+  // The two waves of a key tile's 32 keys swap: the first takes dK's sums of both,
+  // the second dV's; then each stores its own.
+  static_assert(QW == 2 && NW * DT * 4096 <= (int)sizeof(smem), "");
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  auto finish = [&](f32x16(&mine_)[DT], const f32x16(&other)[DT], int which) {
+    f32x4* const to = reinterpret_cast<f32x4*>(smem) + wave * DT * 256 + lane;
+#pragma unroll
+    for (int x = 0; x < 4 * DT; ++x)
+      to[64 * x] = f32x4{other[x >> 2][4 * (x & 3)], other[x >> 2][4 * (x & 3) + 1], other[x >> 2][4 * (x & 3) + 2],
+                         other[x >> 2][4 * (x & 3) + 3]};
+    __syncthreads();
+    const int from = kw + KW * (1 - qw);
+    const f32x4* const in = reinterpret_cast<const f32x4*>(smem) + from * DT * 256 + lane;
+#pragma unroll
+    for (int x = 0; x < 4 * DT; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mine_[x >> 2][4 * (x & 3) + e] += in[64 * x][e];
+    if (p.splits > 1) {
+      f32x4* const g = attn_part<DP>(p, split, kt, BK) + (2 * kw + which) * DT * 256 + lane;
+#pragma unroll
+      for (int x = 0; x < 4 * DT; ++x)
+        g[64 * x] = f32x4{mine_[x >> 2][4 * (x & 3)], mine_[x >> 2][4 * (x & 3) + 1], mine_[x >> 2][4 * (x & 3) + 2],
+                          mine_[x >> 2][4 * (x & 3) + 3]};
+    } else {
+      OT* const g = (OT*)(which ? p.dV : p.dK) + (sq.k0 + key) * (which ? p.ldv : p.ldk) + kvh * (which ? p.hv : p.hk);
+      store_row<DP>(g, key < sq.lk, mine_, which ? 1.0f : p.scale, p.dim, half);
+    }
+  };
+  if (qw == 0) finish(dk, dv, 0);
+  else finish(dv, dk, 1);
 }
 
-// dK and dV from the splits' sums, in split order: DP / 2 threads a key,
-// blockIdx.y the keys of the tile in turn.
+// dK and dV from the splits' sums, in split order: a wave takes 16 values of 32 keys,
+// blockIdx.y four such parts of the tile in turn.
 template <typename OT, int DP, int BK>
 __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs p) {
-  constexpr int KEYS = 256 / (DP / 2);
   const KeyTile kt = attn_key_tile<false>(p, (int)blockIdx.x, BK);
-  const int r = KEYS * blockIdx.y + threadIdx.x / (DP / 2);
-  if (kt.k0 < 0 || r >= BK || kt.k0 + r >= kt.s.lk) return;
-  const int x = 4 * (threadIdx.x % (DP / 2)), d = x % DP;
-  const int64_t key = kt.s.k0 + kt.k0 + r;
-  const f32x4 o = sum_parts4(p.part, p.k_tokens * p.kv * 2 * DP, p.splits, (kt.kvh * p.k_tokens + key) * 2 * DP + x);
-  if (d >= p.dim) return;
-  if (x < DP)
-    store_4((OT*)p.dK + key * p.ldk + kt.kvh * p.hk + d, o[0] * p.scale, o[1] * p.scale, o[2] * p.scale, o[3] * p.scale);
-  else
-    store_4((OT*)p.dV + key * p.ldv + kt.kvh * p.hv + d, o[0], o[1], o[2], o[3]);
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int x = __builtin_amdgcn_readfirstlane(4 * blockIdx.y + (threadIdx.x >> 6));   // 32 keys, matrix, 16 values
+  const int kw = x / (DP / 8), which = x / (DP / 16) % 2, d = 16 * (x % (DP / 16)), key = kt.k0 + 32 * kw + (lane & 31);
+  if (kt.k0 < 0 || kt.k0 + 32 * kw >= kt.s.lk) return;
+  const int64_t step = (int64_t)p.kv * p.tiles * (BK * 2 * DP);
+  const int64_t at = 4 * (attn_part<DP>(p, 0, kt, BK) - reinterpret_cast<f32x4*>(p.part) + 128 * x + lane);
+  const f32x4 a = sum_parts4(p.part, step, p.splits, at), b = sum_parts4(p.part, step, p.splits, at + 256);
+  OT* const g = (OT*)(which ? p.dV : p.dK) + (kt.s.k0 + key) * (which ? p.ldv : p.ldk) + kt.kvh * (which ? p.hv : p.hk);
+  store_pair(g, key < kt.s.lk, d, a, b, which ? 1.0f : p.scale, p.dim, half);
 }
 
 }  // namespace lora
