@@ -151,8 +151,8 @@ int64_t bwd_keys(const lora_attention* a) { return a->dtype == LORA_BF16 && a->h
 // Blocks that share a key tile's rows: enough for causal tiles, whose rows differ
 // by the length of the sequence, to even out over the chip (2048 tokens of 32/8
 // heads of 128 with one, two, three and four rounds of blocks: 120, 91, 108 and 113
-// us, and 12 to 21 for the join; 7 sequences in 4001 of 32/4 heads of 64 with three,
-// four and six: 60, 52 and 58).
+// us when this was chosen, and 12 to 21 for the join; 7 sequences in 4001 of 32/4
+// heads of 64 with three, four and six: 60, 52 and 58).
 struct BwdPlan {
   int64_t tiles, splits;
 };

@@ -31,7 +31,7 @@ struct AttnArgs {
   float* lse;                   // [heads][q_tokens], forward: may be NULL
   float* stat;                  // backward: [2][kv][q_tokens G] log-sums (powers of two) and -delta
   void* dO16;                   // backward, bf16 with float32 dO: dO rounded, [kv][q_tokens G][DP]
-  float *part, *ml;             // splits: sums [splits][kv][q_tokens G][DP], maximum and weight [..][2]
+  float *part, *ml;             // splits: sums [splits][kv][q_tokens G][DP] (backward: attn_part), maximum and weight [..][2]
   const int32_t *qo, *ko, *kl;  // offsets [seqs + 1] and lengths [seqs] or NULL
   int64_t ldq, hq, ldk, hk, ldv, hv, ldo, ho;
   int64_t q_tokens, k_tokens;
@@ -445,13 +445,14 @@ LORA_DEV RowTile attn_row_tile(const AttnArgs& p, int b, int BM) {
 // two): the weights then stay under 2^8 and nothing is lost, and most stages
 // rescale no sums.
 //
-// Measured (32/8 heads of 128, bf16, causal): 4096 tokens 150 us, 8192 520 (0.92
-// and 1.06 PFLOP/s; torch's product of 8192^3 reaches 1.07), 9 sequences in 4001
-// tokens 43; 32 tokens over cold caches of up to 4096 keys 61 with the join (4.2
+// Measured (32/8 heads of 128, bf16, causal): 4096 tokens 146-152 us, 8192 510-535
+// (1.08 PFLOP/s at best; torch's product of 8192^3 reaches 1.07 to 1.22 by the box), 9
+// sequences in 4001 tokens 43; 32 tokens over cold caches of up to 4096 keys 61 with the join (4.2
 // TB/s).  Long sequences are bound by power: the matrix cores are busy for 54 % of
 // the cycles at 1.9 GHz, vector work for most of the others, LDS for a quarter
 // with no bank conflicts, and no order of products, LDS reads, wave priorities or
-// tiles that was tried moved the time.  Short ones are bound by the latency of a
+// tiles that was tried moved the time (nor did blocks of eight waves, which share
+// the keys by twos: 2048 tokens 49 us against 50.5, 4096 162 against 153).  Short ones are bound by the latency of a
 // block's start (offsets, then Q and the first keys) and rounds partly filled.  64
 // keys a stage and two blocks of four waves a CU: at 256 registers two waves a
 // SIMD compute and weigh at different times.
@@ -671,10 +672,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
 // its error in 64 bits 2.3e-3 of which bf16's own rounding is 1.7e-3, against 2.9e-3.
 // dk's and dv's stay within 1.5 times bf16's rounding with one.
 //
-// Measured (32/8 heads of 128, bf16, causal): 2048 tokens 184 us (dQ 92, dK and dV
-// 91, their join 13), 4096 565 (264, 280, 21); over all keys the passes run at 1.04
-// and 0.89 PFLOP/s of products done, so that what is left at 2048 is causal tiles
-// that do not fill the last round.
+// Measured (32/8 heads of 128, bf16, causal): 2048 tokens 172-177 us (dQ 85-90, dK and
+// dV 88, their join 14), 4096 545 (245, 278, 22), 9 sequences in 4001 tokens 165 (71,
+// 72, 23); 32/4 heads of 64, 7 sequences in 4001 tokens 89.  Over all keys the
+// passes run at 1.09 and 0.92 PFLOP/s of the products they do; what is left at 2048
+// is causal tiles that do not fill the last round, and the splits' sums (67 MB
+// written and read).
 // ---------------------------------------------------------------------------
 // The block's sequence and key tile.
 struct KeyTile {
@@ -848,7 +851,8 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 ? 2 : 1) void attn_dq_
 // with their log-sums and deltas.  p.splits blocks share a key tile's stages where
 // there are few tiles.  (The stages of all tiles in equal runs, one a block, would
 // balance causal tiles exactly, but blocks then read rows far apart and L2 no
-// longer holds what they share: 2048 tokens 123 us against 104 then.)
+// longer holds what they share: 2048 tokens 123 us against 104 then.  Short tiles
+// in fewer parts save sums, but leave long parts for the end: 96 against 88.)
 template <typename T, typename OT, int DP, int KW, int QW, int QT>
 __global__ __launch_bounds__(64 * KW * QW, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(AttnArgs p) {
   constexpr int NW = KW * QW, BK = 32 * KW, BQ = 32 * QW * QT, KS = DP / Frag<T>::FK, DT = DP / 32;
@@ -869,8 +873,9 @@ __global__ __launch_bounds__(64 * KW * QW, sizeof(T) == 2 ? 2 : 1) void attn_dkv
   const int kw = wave % KW, qw = wave / KW;
   const int key = k0 + 32 * kw + (lane & 31), kc = min(key, sq.lk - 1);
   // bf16 at DP 128: K and V stay in LDS, which leaves the registers for two waves a
-  // SIMD (2048 tokens of 32/8 heads: 91 us); one wave with them in registers keeps
-  // the matrix cores busy for 42 % of its cycles and LDS for a quarter (104 us).
+  // SIMD (2048 tokens of 32/8 heads then 91 us; K alone in registers the same); one
+  // wave with both in registers keeps the matrix cores busy for 42 % of its cycles and
+  // LDS for a quarter (104 us).
   const T* const Kg = (const T*)p.K + (sq.k0 + k0) * p.ldk + kvh * p.hk;
   const T* const Vg = (const T*)p.V + (sq.k0 + k0) * p.ldv + kvh * p.hv;
   lds_char* const Kl = lds + 2 * STAGE;
