@@ -29,6 +29,14 @@ def test_caches_of_a_large_batch(dtype):
     check([70] * 12, [100] * 12, 32, 32, 64, True, dtype, dtype, lens=[100, 70, 75, 99, 71, 70, 80, 90, 73, 74, 100, 0])
 
 
+# more sequences than a wave has lanes, each long enough for its key tiles to be shared
+@pytest.mark.parametrize("dtype,out", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_shared_key_tiles_of_many_sequences(D, dtype, out):
+    lens = [40 + (i * 11) % 31 for i in range(66)]
+    check(lens, [n + i % 2 for i, n in enumerate(lens)], 8, 1, D, True, dtype, out)
+
+
 def both(at, q, k, v, do, out):
     """A call on any stream with everything it writes made beforehand."""
     o, lse, dq, dk, dv = out
