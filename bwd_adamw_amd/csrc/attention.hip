@@ -92,8 +92,12 @@ double attn_bytes(const lora_attention* a, int n) {
 // more than 32 rows (single tokens: blocks of their own, which load and compute at
 // different times, read cold caches of 32 requests up to 4096 keys at 4.2 TB/s,
 // four waves in step at 3.8).  Then the blocks that share a row tile's keys, so
-// that few rows still fill the chip: 128 keys each at least for single tokens,
-// else 256 (by the sequences' mean room: lengths are known to the kernels only).
+// that few rows still fill the chip, by the sequences' mean room (lengths are known
+// to the kernels only): 256 keys each at least, 128 for single tokens (64: one over
+// 4000 keys 14.6 us against 13), 32 in float32, whose products take 2 to 4 us a
+// stage (one over 300 keys, head size 64: 12.7 us against 20 with 128); and no more
+// than run at once (float32 of head size 128: 4 a CU; 8 tokens over 2000 keys 47 us
+// against 51 with 8).
 struct FwdPlan {
   int rw;                  // waves of 32 rows
   int64_t tiles, splits;
@@ -106,7 +110,9 @@ FwdPlan fwd_plan(const lora_attention* a) {
                                                                              : 4;
   f.tiles = tile_count(a->q_tokens, group, a->seqs, 32 * f.rw);
   const int64_t blocks = f.tiles * a->kv_heads;
-  f.splits = f.rw == 1 ? clampi(cdiv(8 * kCUs, blocks), 1, clampi(room / 128, 1, 64))
+  const bool f32 = a->dtype == LORA_F32;
+  const int64_t most = (f32 && a->head_dim > 64 ? 4 : 8) * kCUs, least = f32 ? 32 : 128;
+  f.splits = f.rw == 1 ? clampi(cdiv(most, blocks), 1, clampi(room / least, 1, 64))
              : blocks < kCUs ? clampi(cdiv(4 * kCUs, blocks), 1, clampi(room / 256, 1, 64))
                              : 1;
   return f;

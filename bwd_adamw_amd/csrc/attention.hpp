@@ -462,8 +462,12 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 && CW == 1 ? 2 : 1) vo
   constexpr int NW = RW * CW, BM = 32 * RW, BN = 32 * KT * CW, KS = DP / Frag<T>::FK, DT = DP / 32;
   typedef typename Frag<T>::V V;
   typedef Tile<T, DP, BN, NW> Ti;
-  constexpr int STAGE = 2 * Ti::BYTES, MERGE = CW > 1 ? NW * (DT * 4096 + 512) : 0;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE > MERGE ? 2 * STAGE : MERGE];
+  // Single tokens in float32: one stage in LDS, and twice the blocks a CU load and
+  // compute at different times (8 tokens over 2000 keys, 32/8 heads of 128: 63 us with
+  // two stages, 47; bf16, whose stages are half as large, 61 with two and 67).
+  constexpr bool ONE = NW == 1 && sizeof(T) == 4;
+  constexpr int STAGE = 2 * Ti::BYTES, ALL = (ONE ? 1 : 2) * STAGE, MERGE = CW > 1 ? NW * (DT * 4096 + 512) : 0;
+  __shared__ __attribute__((aligned(1024))) char smem[ALL > MERGE ? ALL : MERGE];
   lds_char* const lds = (lds_char*)smem;
   const int split = (int)(blockIdx.x / p.kv) % p.splits;
   const RowTile rt = attn_row_tile<(RW == 2)>(p, (int)(blockIdx.x / p.kv / p.splits) * p.kv + (int)(blockIdx.x % p.kv), BM);
@@ -508,7 +512,7 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 && CW == 1 ? 2 : 1) vo
   auto step = [&](int st, auto B) {
     constexpr int buf = decltype(B)::value;
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (st + 1 < st1) load(buf ^ 1);
+    if (!ONE && st + 1 < st1) load(buf ^ 1);
     lds_char* const Ks = lds + buf * STAGE;
     lds_char* const Vs = Ks + Ti::BYTES;
     const int kb = st * BN + 32 * KT * cw;
@@ -548,9 +552,17 @@ __global__ __launch_bounds__(64 * RW * CW, sizeof(T) == 2 && CW == 1 ? 2 : 1) vo
   };
   if (st0 < st1) load(0);
   wait_loads();   // Q too: a wait that the compiler placed in the loop would hold up the stages
-  for (int st = st0; st < st1; st += 2) {
-    step(st, std::integral_constant<int, 0>{});
-    if (st + 1 < st1) step(st + 1, std::integral_constant<int, 1>{});
+  if constexpr (ONE) {
+    for (int st = st0; st < st1; ++st) {
+      step(st, std::integral_constant<int, 0>{});
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage is read
+      if (st + 1 < st1) load(0);
+    }
+  } else {
+    for (int st = st0; st < st1; st += 2) {
+      step(st, std::integral_constant<int, 0>{});
+      if (st + 1 < st1) step(st + 1, std::integral_constant<int, 1>{});
+    }
   }
   l += other_half(l);
   if constexpr (CW > 1) {
