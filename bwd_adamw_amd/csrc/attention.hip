@@ -93,9 +93,10 @@ double attn_bytes(const lora_attention* a, int n) {
 // different times, read cold caches of 32 requests up to 4096 keys at 4.2 TB/s,
 // four waves in step at 3.8).  Then the blocks that share a row tile's keys, so
 // that few rows still fill the chip, by the sequences' mean room (lengths are known
-// to the kernels only): 256 keys each at least, 128 for single tokens (64: one over
-// 4000 keys 14.6 us against 13), 32 in float32, whose products take 2 to 4 us a
-// stage (one over 300 keys, head size 64: 12.7 us against 20 with 128); and no more
+// to the kernels only): 256 keys each at least (100 tokens over 2000, 32/8 heads: 20 us
+// against 25 with 128), 128 for single tokens (64: one over 4000 keys 14.6 us against
+// 13).  In float32, whose products take 2 to 4 us a stage, 128 (20 tokens over 2000: 27
+// us against 36) and 32 (one over 300, head size 64: 13 us against 20).  And no more
 // than run at once (float32 of head size 128: 4 a CU; 8 tokens over 2000 keys 47 us
 // against 51 with 8).
 struct FwdPlan {
@@ -113,7 +114,7 @@ FwdPlan fwd_plan(const lora_attention* a) {
   const bool f32 = a->dtype == LORA_F32;
   const int64_t most = (f32 && a->head_dim > 64 ? 4 : 8) * kCUs, least = f32 ? 32 : 128;
   f.splits = f.rw == 1 ? clampi(cdiv(most, blocks), 1, clampi(room / least, 1, 64))
-             : blocks < kCUs ? clampi(cdiv(4 * kCUs, blocks), 1, clampi(room / 256, 1, 64))
+             : blocks < kCUs ? clampi(cdiv(4 * kCUs, blocks), 1, clampi(room / (f32 ? 128 : 256), 1, 64))
                              : 1;
   return f;
 }
