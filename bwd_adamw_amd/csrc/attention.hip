@@ -86,10 +86,20 @@ double attn_bytes(const lora_attention* a, int n) {
   return a->head_dim * (a->q_tokens * a->heads * (e + n * oe) + a->k_tokens * a->kv_heads * (2 * e + (n > 1 ? 2 * oe : 0)));
 }
 
+// Whether a block takes two waves of 32 rows, times two that share a stage's keys,
+// where it would take four of rows: in bf16 where four would leave CUs idle (2048
+// tokens of 32/8 heads of 128, two rounds: forward 63 us with two and two, 55 with four,
+// dQ over all keys 150 and 132).  In float32 up to the causal tiles of two or three
+// rounds, which half as long blocks even out (4096 tokens of 8 heads of 64: forward 293
+// -> 212, dQ 394 -> 228, 8192 forward 784 -> 625; 2048 of 32/8 heads of 128, four
+// rounds, 325 -> 400).
+bool few_rows(const lora_attention* a) {
+  const int64_t rounds = a->dtype == LORA_BF16 ? 1 : a->head_dim > 64 ? 2 : 3;
+  return tile_count(a->q_tokens, a->heads / a->kv_heads, a->seqs, 128) * a->kv_heads < rounds * kCUs;
+}
+
 // The forward's kernel: four waves of 32 rows a block; two, times two that share
-// a stage's keys, where four would leave CUs idle (beyond that four are faster: 2048
-// tokens of 32/8 heads 55 us against 63); one where a sequence has no
-// more than 32 rows (single tokens: blocks of their own, which load and compute at
+// a stage's keys, for few rows; one where a sequence has no more than 32 rows (single tokens: blocks of their own, which load and compute at
 // different times, read cold caches of 32 requests up to 4096 keys at 4.2 TB/s,
 // four waves in step at 3.8).  Then the blocks that share a row tile's keys, so
 // that few rows still fill the chip, by the sequences' mean room (lengths are known
@@ -106,9 +116,7 @@ struct FwdPlan {
 FwdPlan fwd_plan(const lora_attention* a) {
   const int64_t group = a->heads / a->kv_heads, room = a->k_tokens / a->seqs;
   FwdPlan f;
-  f.rw = a->q_tokens * group <= 32 * a->seqs                                     ? 1
-         : tile_count(a->q_tokens, group, a->seqs, 128) * a->kv_heads < kCUs ? 2
-                                                                             : 4;
+  f.rw = a->q_tokens * group <= 32 * a->seqs ? 1 : few_rows(a) ? 2 : 4;
   f.tiles = tile_count(a->q_tokens, group, a->seqs, 32 * f.rw);
   const int64_t blocks = f.tiles * a->kv_heads;
   const bool f32 = a->dtype == LORA_F32;
@@ -193,10 +201,7 @@ void backward(const lora_attention* a, AttnArgs p, void* ws, hipStream_t st) {
   p.stat = (float*)ws;
   p.dO16 = (char*)ws + w.dO16;
   p.part = (float*)((char*)ws + w.part);
-  // Two rows' waves a block, times two that share the keys, where four would leave
-  // CUs idle (2048 tokens of 32/8 heads, two rounds of blocks: 150 us so over all
-  // keys, 132 with four; 4 x 128 of 32/4 heads float32: 15 against 20).
-  const bool small = tile_count(a->q_tokens, p.group, a->seqs, 128) * p.kv < kCUs;
+  const bool small = few_rows(a);
   {
     p.tiles = (int32_t)tile_count(a->q_tokens, p.group, a->seqs, small ? 64 : 128);
     prof::Scope ps("attn_dq", a->q_tokens, a->k_tokens, a->heads, 6.0 * a->head_dim * attn_pairs(a), attn_bytes(a, 3));

@@ -29,6 +29,13 @@ def test_caches_of_a_large_batch(dtype):
     check([70] * 12, [100] * 12, 32, 32, 64, True, dtype, dtype, lens=[100, 70, 75, 99, 71, 70, 80, 90, 73, 74, 100, 0])
 
 
+# three rounds of blocks of 128 rows and more, where float32 takes four row tiles a block too
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", [([200, 130], [200, 140], 256, 256, 64), ([200, 130], [190, 130], 256, 128, 128)], ids=str)
+def test_larger_batches_in_float32(case, causal):
+    check(*case, causal, F32, F32)
+
+
 # more sequences than a wave has lanes, each long enough for its key tiles to be shared
 @pytest.mark.parametrize("dtype,out", TYPES)
 @pytest.mark.parametrize("D", [64, 128])
