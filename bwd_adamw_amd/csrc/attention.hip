@@ -87,14 +87,16 @@ double attn_bytes(const lora_attention* a, int n) {
 }
 
 // Whether a block takes two waves of 32 rows, times two that share a stage's keys,
-// where it would take four of rows: in bf16 where four would leave CUs idle (2048
-// tokens of 32/8 heads of 128, two rounds: forward 63 us with two and two, 55 with four,
-// dQ over all keys 150 and 132).  In float32 up to the causal tiles of two or three
-// rounds, which half as long blocks even out (4096 tokens of 8 heads of 64: forward 293
-// -> 212, dQ 394 -> 228, 8192 forward 784 -> 625; 2048 of 32/8 heads of 128, four
-// rounds, 325 -> 400).
+// where it would take four of rows: where four would leave CUs idle, and up to two
+// rounds of blocks (float32 of head sizes to 64: three) where the causal tiles of long
+// sequences leave the last round uneven, which half as long blocks even out.  Measured
+// with four and with two and two: bf16 of 8 heads of 128, 4096 tokens, forward 83 us
+// and 73, dQ 127 and 89, of 32/8 heads, 1024 tokens, 26 and 25, 39 and 31, but 5
+// sequences of 300 16 and 22, 23 and 28, and 2048 tokens, two rounds and over, 55 and
+// 63, 94 and 95; float32 of 8 heads of 64, 4096 tokens, 293 and 212, 394 and 228, of
+// 32/8 of 128, 2048 tokens, 325 and 400.
 bool few_rows(const lora_attention* a) {
-  const int64_t rounds = a->dtype == LORA_BF16 ? 1 : a->head_dim > 64 ? 2 : 3;
+  const int64_t rounds = a->dtype == LORA_F32 ? (a->head_dim > 64 ? 2 : 3) : a->k_tokens / a->seqs >= 1024 ? 2 : 1;
   return tile_count(a->q_tokens, a->heads / a->kv_heads, a->seqs, 128) * a->kv_heads < rounds * kCUs;
 }
 

@@ -36,6 +36,13 @@ def test_larger_batches_in_float32(case, causal):
     check(*case, causal, F32, F32)
 
 
+# one long sequence in up to two rounds of blocks: two row tiles a block, in bf16 too
+@pytest.mark.parametrize("dtype,out", TYPES)
+@pytest.mark.parametrize("case", [([1100], [1100], 34, 34, 64), ([1030], [1100], 36, 36, 128)], ids=str)
+def test_long_sequences_of_few_blocks(case, dtype, out):
+    check(*case, True, dtype, out)
+
+
 # more sequences than a wave has lanes, each long enough for its key tiles to be shared
 @pytest.mark.parametrize("dtype,out", TYPES)
 @pytest.mark.parametrize("D", [64, 128])
