@@ -580,7 +580,8 @@ int lora_heads_backward(int n, const lora_heads* heads, const void* const* X, co
  * aligned (LORA_E_ALIGN); heads is a multiple of kv_heads, q_tokens heads,
  * k_tokens and seqs heads are below 2^30, ldk and ldv at most 2^22, and
  * heads / kv_heads hq + 128 ldq (and the same of O) below 2^29 (LORA_E_SHAPE).
- * Outputs must not overlap inputs. */
+ * Outputs must not overlap inputs or each other (LORA_E_INVALID where two start
+ * at the same place). */
 typedef struct lora_attention {
   int64_t q_tokens, k_tokens;   /* rows of Q and of K and V                */
   int64_t heads, kv_heads, head_dim, seqs;

@@ -198,3 +198,22 @@ def test_calls_on_another_device_than_the_current_one_are_refused(monkeypatch):
     monkeypatch.undo()
     torch.cuda.synchronize()
     assert (y == 7.0).all()
+
+
+def test_an_output_in_place_of_an_input_is_refused():
+    bf = torch.bfloat16
+    off = dints([0, 4])
+    at = L.make_attention(4, 4, 2, 2, 64, off, off)
+    q, k, v, o, do, dq, dk, dv = (torch.ones(4, 2, 64, device=DEV, dtype=bf) for _ in range(8))
+    lse = torch.zeros(2, 4, device=DEV)
+    for t in (q, k, v):
+        with pytest.raises(L.LoraError):
+            L.lora_attention_forward(at, q, k, v, t, lse)
+    for i in range(3):
+        for t in (q, k, v, o, do, *[g for j, g in enumerate((dq, dk, dv)) if j != i]):
+            grads = [dq, dk, dv]
+            grads[i] = t
+            with pytest.raises(L.LoraError):
+                L.lora_attention_backward(at, q, k, v, o, do, lse, *grads)
+    torch.cuda.synchronize()
+    assert all((t == 1).all() for t in (q, k, v, o, do, dq, dk, dv))
