@@ -111,6 +111,9 @@ void launch_heads(int lph, const HeadsArgs& a, dim3 grid, hipStream_t st, const 
 #undef LORA_HEADS
 }
 
+// Whether Y may lie over X: a head is then written where it was read.
+bool same_rows(const lora_heads& h) { return h.x_dtype == h.y_dtype && h.ldx == h.ldy && h.hx == h.hy; }
+
 }  // namespace
 
 extern "C" {
@@ -135,6 +138,8 @@ int lora_heads_forward(int n, const lora_heads* heads, const void* const* X, voi
     bytes += e * (size_of(h.x_dtype) + size_of(h.y_dtype));
   }
   if ((uintptr_t)positions & 3u) return LORA_E_ALIGN;
+  for (int i = 0; i < n; ++i)
+    if (X[i] == Y[i] && !same_rows(heads[i])) return LORA_E_INVALID;
   prof::Scope ps("heads_fwd", heads->tokens, heads->heads * heads->head_dim, n, flops, bytes);
   const dim3 grid((unsigned)heads_blocks(n, heads, kFwd), (unsigned)n);
   const int lph = lanes_of(n, heads);
@@ -188,6 +193,8 @@ int lora_heads_backward(int n, const lora_heads* heads, const void* const* X, co
   if ((uintptr_t)positions & 3u) return LORA_E_ALIGN;
   const size_t need = sums ? lora_heads_workspace_bytes(n, heads) : 0;
   if (need && (!ws || ws_bytes < need || !al16(ws))) return LORA_E_WORKSPACE;
+  for (int i = 0; i < n; ++i)
+    if (a.one[i].out == a.one[i].dY && !same_rows(heads[i])) return LORA_E_INVALID;
   hipStream_t st = (hipStream_t)stream;
   {
     prof::Scope ps("heads_bwd", heads->tokens, heads->heads * heads->head_dim, n, flops, bytes);

@@ -294,3 +294,11 @@ def test_binding_checks_tensors():
         L.lora_heads_forward([h], [ok.bfloat16()], [ok])
     with pytest.raises(ValueError):
         L.lora_heads_forward([h, h], [ok], [ok])
+
+
+@no_device
+@pytest.mark.parametrize("kw", [dict(y_dtype=L.BF16), dict(ldy=256), dict(ldy=64, hy=256)])
+def test_in_place_with_other_rows_is_refused(kw):
+    arr, ptr, ws = (L.LoraHeads * 1)(_h(**kw)), (C.c_void_p * 1)(256), 1 << 20
+    assert L.lib().lora_heads_forward(1, arr, ptr, ptr, 256, None) == -1
+    assert L.lib().lora_heads_backward(1, arr, (C.c_void_p * 1)(512), ptr, ptr, None, 256, 0, 256, ws, None) == -1
